@@ -80,7 +80,7 @@ class Stats(ctypes.Structure):
                 "n_launches": self.n_launches, "n_text_passes": self.n_text_passes}
 
 
-_vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_vp, _i, _f, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 
 
 def _declare(L: ctypes.CDLL) -> None:
@@ -128,6 +128,10 @@ def _declare(L: ctypes.CDLL) -> None:
                                        _vp]),
         "dvlm_block_attn_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp]),
         "dvlm_engine_set_trace": (_i, [_vp, _vp, _sz, _vp]),
+        "dvlm_page_plan": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 6),
+        "dvlm_mrope": (_i, [_vp, _vp, _vp, _i, _i, _i, _ll, _ll, _i, _i, _vp, _f, _i, _i, _vp, _vp]),
+        "dvlm_mrope_append_paged": (_i, [_vp] * 6 + [_i] * 5 + [_ll, _i, _i, _vp, _f, _i, _vp, _vp]),
+        "dvlm_spec_verify_sample": (_i, [_vp] * 6 + [_i] * 4 + [_vp] * 6),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -260,6 +264,113 @@ def quantize_rows_e4m3(a, codes, scales, *, rows, K, stream=None) -> None:
 def selftest_wait_timeout(budget_cycles: int, status, gave_up, stream=None) -> None:
     _check(lib().dvlm_selftest_wait_timeout(int(budget_cycles), ptr(status), ptr(gave_up), stream_handle(stream)),
            "dvlm_selftest_wait_timeout")
+
+
+# ---------------------------------------------------------------- batched step over paged caches
+def _take(where: str, device, *args) -> None:
+    """Refuse tensors the library would misread: args are (tensor, dtype, least
+    number of elements) triples; all contiguous, all on `device`."""
+    for t, dtype, least in args:
+        if t is not None and (t.dtype != dtype or t.numel() < least or t.device != device or not t.is_contiguous()):
+            raise DvlmError(1, f"{where}: expected a contiguous {dtype} tensor of at least {least} elements on "
+                               f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _launch(fn, where: str, device, stream, *args) -> None:
+    """Call an entry point whose last argument is the stream with the tensors' device current."""
+    import torch
+    if device.type != "cuda":
+        raise DvlmError(1, f"{where}: the tensors are on {device}, not on a GPU")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, stream_handle(stream)), where)
+    else:
+        _check(fn(*args, stream_handle(stream)), where)
+
+
+_sections_cache: dict = {}
+
+
+def _sections(sections):
+    """Host int array of a section list (kept per list: there are only a few)."""
+    key = tuple(sections)
+    arr = _sections_cache.get(key)
+    if arr is None:
+        arr = _sections_cache[key] = (ctypes.c_int * len(key))(*key)
+    return arr
+
+
+def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batch, max_pages, n_pages, max_rows,
+              kv_len, cu_rows, slot_map, free_count_out, status=None, stream=None) -> None:
+    """Block tables, row offsets and slot map of a ragged step (dvlm_page_plan)."""
+    import torch
+    i32, dev = torch.int32, cache_len.device
+    _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
+          (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
+          (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
+          (status, i32, 1))
+    _launch(lib().dvlm_page_plan, "dvlm_page_plan", dev, stream, ptr(cache_len), ptr(new_len), ptr(block_table),
+            ptr(free_pages), ptr(free_count), n_batch, max_pages, n_pages, max_rows, ptr(kv_len), ptr(cu_rows),
+            ptr(slot_map), ptr(free_count_out), ptr(status))
+
+
+def _rows(where: str, t, dtype, rows: int, ld: int, width: int, device) -> int:
+    """Row stride (elements) of a tensor whose rows of `width` elements lie ld apart (0: the
+    tensor's own first stride when it has one row per leading index and dense rows, else width)."""
+    if t.dtype != dtype or t.device != device:
+        raise DvlmError(1, f"{where}: expected a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
+    if not ld:
+        inner = t[0] if t.dim() > 1 and t.shape[0] else t
+        if t.dim() > 1 and t.shape[0] >= rows and inner.numel() >= width and inner.is_contiguous():
+            return int(t.stride(0)) if t.shape[0] > 1 else max(int(inner.numel()), width)
+        ld = width
+    if not t.is_contiguous() or (rows > 0 and t.numel() < (rows - 1) * ld + width):
+        raise DvlmError(1, f"{where}: {tuple(t.shape)} does not hold {rows} rows of {width} elements {ld} apart")
+    return int(ld)
+
+
+def mrope(x, out, pos, *, n_rows, n_heads, D, sections, rope_base, dtype, rot_dim=0, interleaved=0, x_ld=0, out_ld=0,
+          status=None, stream=None) -> None:
+    """Rotary positions with len(sections) axes on rows of heads (dvlm_mrope).  rot_dim 0: D.
+    Row strides 0: taken from the tensors (rows may be slices of wider rows)."""
+    import torch
+    dev, td = x.device, torch.float32 if dtype == DVLM_FP32 else torch.bfloat16
+    x_ld = _rows("dvlm_mrope", x, td, n_rows, x_ld, n_heads * D, dev)
+    out_ld = _rows("dvlm_mrope", out, td, n_rows, out_ld, n_heads * D, dev)
+    sec = _sections(sections)
+    _take("dvlm_mrope", dev, (pos, torch.int32, len(sec) * n_rows), (status, torch.int32, 1))
+    _launch(lib().dvlm_mrope, "dvlm_mrope", dev, stream, ptr(x), ptr(out), ptr(pos), n_rows, n_heads, D, x_ld, out_ld,
+            rot_dim or D, len(sec), sec, float(rope_base), int(interleaved), dtype, ptr(status))
+
+
+def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, Hq, Hkv, D, n_pages, sections,
+                       rope_base, rot_dim=0, interleaved=0, qkv_ld=0, status=None, stream=None) -> None:
+    """Rotate queries and keys and write keys and values into their pages (dvlm_mrope_append_paged)."""
+    import torch
+    dev, bf = qkv.device, torch.bfloat16
+    qkv_ld = _rows("dvlm_mrope_append_paged", qkv, bf, n_rows, qkv_ld, (Hq + 2 * Hkv) * D, dev)
+    sec = _sections(sections)
+    _take("dvlm_mrope_append_paged", dev, (pos, torch.int32, len(sec) * n_rows), (slot_map, torch.int32, n_rows),
+          (q_out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D), (v_pages, bf, n_pages * Hkv * 64 * D),
+          (status, torch.int32, 1))
+    _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, ptr(qkv), ptr(pos), ptr(slot_map),
+            ptr(q_out), ptr(k_pages), ptr(v_pages), n_rows, Hq, Hkv, D, n_pages, qkv_ld, rot_dim or D, len(sec), sec,
+            float(rope_base), int(interleaved), ptr(status))
+
+
+def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K, V, dtype, accept_len, out_ids,
+                       n_draft=None, cache_len=None, cache_len_out=None, status=None, stream=None) -> None:
+    """Verify drafts by rejection sampling with given random numbers (dvlm_spec_verify_sample)."""
+    import torch
+    dev, i32, f32 = target_p.device, torch.int32, torch.float32
+    td = f32 if dtype == DVLM_FP32 else torch.bfloat16
+    _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
+          (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),
+          (accept_len, i32, b), (out_ids, i32, b * (K + 1)), (cache_len, i32, b), (cache_len_out, i32, b),
+          (status, i32, 1))
+    _launch(lib().dvlm_spec_verify_sample, "dvlm_spec_verify_sample", dev, stream, ptr(target_p), ptr(draft_p),
+            ptr(draft_ids), ptr(n_draft), ptr(u_accept), ptr(u_sample), b, K, V, dtype, ptr(accept_len), ptr(out_ids),
+            ptr(cache_len), ptr(cache_len_out), ptr(status))
 
 
 # ---------------------------------------------------------------- engine

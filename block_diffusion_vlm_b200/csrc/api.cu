@@ -400,6 +400,107 @@ dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const int32_t* ve
                                      n_layers, Hkv, D, Lmax, dev_status, cs(stream)));
 }
 
+// ------------------------------------------------------------ batched step over paged caches
+namespace {
+// Largest page count whose slot numbers (page * 64 + row) stay in 31 bits.
+constexpr int kMaxPages = (1 << 25) - 1;
+
+dvlm_status mrope_axes(MropeAxes* ax, const int32_t* pos, int n_axes, const int* sections, int rot_dim, int D,
+                       float rope_base, int interleaved) {
+  if (!pos || !sections || !std::isfinite(rope_base) || !(rope_base > 0.f)) return DVLM_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return DVLM_ERR_INVALID_ARG;
+  if (n_axes < 1 || n_axes > kMropeMaxAxes || rot_dim < 2 || rot_dim > D || rot_dim % 2) return DVLM_ERR_SHAPE;
+  long long sum = 0;
+  ax->pos = pos;
+  ax->n = n_axes;
+  for (int i = 0; i < n_axes; ++i) {
+    if (sections[i] < 0) return DVLM_ERR_SHAPE;
+    ax->section[i] = sections[i];
+    sum += sections[i];
+  }
+  if (sum != rot_dim / 2) return DVLM_ERR_SHAPE;
+  ax->interleaved = interleaved;
+  ax->rot = rot_dim;
+  ax->log2_base = std::log2(static_cast<double>(rope_base));
+  return DVLM_OK;
+}
+}  // namespace
+
+dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
+                           int32_t* free_pages, const int32_t* free_count, int n_batch, int max_pages, int n_pages,
+                           int max_rows, int32_t* kv_len, int32_t* cu_rows, int32_t* slot_map,
+                           int32_t* free_count_out, int* dev_status, dvlm_stream stream) {
+  if (!cache_len || !new_len || !block_table || !free_pages || !free_count || !kv_len || !cu_rows || !slot_map ||
+      !free_count_out)
+    return DVLM_ERR_INVALID_ARG;
+  if (n_batch < 1 || n_batch > kPlanMaxBatch || max_pages < 1 || max_pages > kMaxPages || n_pages < 1 ||
+      n_pages > kMaxPages || max_rows < 1)
+    return DVLM_ERR_SHAPE;
+  PagePlanArgs a{cache_len, new_len, block_table, free_pages, free_count, n_batch, max_pages, n_pages, max_rows,
+                 kv_len, cu_rows, slot_map, free_count_out, dev_status};
+  return cuda_status(launch_page_plan(a, cs(stream)));
+}
+
+dvlm_status dvlm_mrope(const void* x, void* out, const int32_t* pos, int n_rows, int n_heads, int D, long long x_ld,
+                       long long out_ld, int rot_dim, int n_axes, const int* sections, float rope_base,
+                       int interleaved, dvlm_dtype dt, int* dev_status, dvlm_stream stream) {
+  (void)dev_status;
+  if (!x || !out || (dt != DVLM_BF16 && dt != DVLM_FP32)) return DVLM_ERR_INVALID_ARG;
+  const uintptr_t es = dt == DVLM_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es) return DVLM_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_heads < 1 || n_heads > 65535 || D < 2 || D > 256) return DVLM_ERR_SHAPE;
+  const long long width = static_cast<long long>(n_heads) * D;
+  if (x_ld < width || out_ld < width || width > (1 << 24) || (x == out && x_ld != out_ld)) return DVLM_ERR_SHAPE;
+  MropeAxes ax{};
+  const dvlm_status st = mrope_axes(&ax, pos, n_axes, sections, rot_dim, D, rope_base, interleaved);
+  if (st != DVLM_OK) return st;
+  return cuda_status(launch_mrope_rows(x, out, x_ld, out_ld, n_rows, n_heads, D, dt == DVLM_BF16, ax, cs(stream)));
+}
+
+dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos, const int32_t* slot_map, void* q_out,
+                                    void* k_pages, void* v_pages, int n_rows, int Hq, int Hkv, int D, int n_pages,
+                                    long long qkv_ld, int rot_dim, int n_axes, const int* sections, float rope_base,
+                                    int interleaved, int* dev_status, dvlm_stream stream) {
+  if (!qkv || !slot_map || !q_out || !k_pages || !v_pages) return DVLM_ERR_INVALID_ARG;
+  if (!al16(qkv) || !al16(q_out) || !al16(k_pages) || !al16(v_pages)) return DVLM_ERR_INVALID_ARG;
+  if (n_rows < 1 || Hq < 1 || Hkv < 1 || Hq > 4096 || Hkv > 4096 || n_pages < 1 || n_pages > kMaxPages || D < 1)
+    return DVLM_ERR_SHAPE;
+  if (D != 64 && D != 128) return DVLM_ERR_UNSUPPORTED;
+  if (qkv_ld < static_cast<long long>(Hq + 2 * Hkv) * D || qkv_ld % 8) return DVLM_ERR_SHAPE;
+  MropeAppendArgs a{};
+  const dvlm_status st = mrope_axes(&a.ax, pos, n_axes, sections, rot_dim, D, rope_base, interleaved);
+  if (st != DVLM_OK) return st;
+  a.qkv = static_cast<const bf16*>(qkv);
+  a.qkv_ld = qkv_ld;
+  a.q_out = static_cast<bf16*>(q_out);
+  a.k_pages = static_cast<bf16*>(k_pages);
+  a.v_pages = static_cast<bf16*>(v_pages);
+  a.slot_map = slot_map;
+  a.n_rows = n_rows;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.n_pages = n_pages;
+  a.status = dev_status;
+  return cuda_status(launch_mrope_append(a, D, cs(stream)));
+}
+
+dvlm_status dvlm_spec_verify_sample(const void* target_p, const void* draft_p, const int32_t* draft_ids,
+                                    const int32_t* n_draft, const float* u_accept, const float* u_sample, int b, int K,
+                                    int V, dvlm_dtype dt, int32_t* accept_len, int32_t* out_ids,
+                                    const int32_t* cache_len, int32_t* cache_len_out, int* dev_status,
+                                    dvlm_stream stream) {
+  if (!target_p || !draft_ids || !u_accept || !u_sample || !accept_len || !out_ids) return DVLM_ERR_INVALID_ARG;
+  if ((cache_len != nullptr) != (cache_len_out != nullptr)) return DVLM_ERR_INVALID_ARG;
+  if (dt != DVLM_BF16 && dt != DVLM_FP32) return DVLM_ERR_INVALID_ARG;
+  const uintptr_t es = dt == DVLM_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(target_p) % es || reinterpret_cast<uintptr_t>(draft_p) % es)
+    return DVLM_ERR_INVALID_ARG;
+  if (b < 1 || b > 65535 || K < 1 || K > 64 || V < 1 || V > (1 << 30)) return DVLM_ERR_SHAPE;
+  SpecSampleArgs a{target_p, draft_p, draft_ids, n_draft, u_accept, u_sample, b, K, V,
+                   accept_len, out_ids, cache_len, cache_len_out, dev_status};
+  return cuda_status(launch_spec_sample(a, dt == DVLM_BF16, cs(stream)));
+}
+
 // ------------------------------------------------------------ FP8 weights
 dvlm_status dvlm_quantize_rows_e4m3(const void* a, int rows, int K, uint8_t* codes, float* scales,
                                     dvlm_stream stream) {

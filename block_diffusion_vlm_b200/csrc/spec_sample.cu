@@ -1,0 +1,273 @@
+// Verification of drafted tokens by rejection sampling, from given uniform
+// random numbers.
+//
+// Mathematics: draft x_j is accepted while u_j q_j(x_j) < p_j(x_j) (u in
+// [0, 1)); at the first rejection k the next token is drawn from the residual
+// r = max(p_k - q_k, 0), after K acceptances from r = p_K.  The draw inverts
+// the cumulative sum: the lowest v with C(v) > u C(V - 1).  Accepted and drawn
+// tokens together are distributed as the target's own samples.  The products
+// u q are exact in fp64 (24 x 24 bits), and so is the decision; C is summed
+// in fp64, so that it is the same token whatever the order of the sum unless
+// u C lies within about 1e-13 of a step.
+//
+// Bound: HBM in batches (one target row, and the draft's row where it has
+// probabilities, per sequence: the K + 1 rows are never read whole), latency
+// alone.  One cluster per sequence: each of its warps owns a contiguous
+// stretch of the vocabulary and sums it, the CTA totals meet in distributed
+// shared memory, and the one warp whose stretch holds the step walks it again
+// out of L2.  No scratch, no atomics: sums in a fixed order.
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dvlm {
+
+namespace {
+constexpr int kSvThreads = 512;
+constexpr int kSvWarps = kSvThreads / 32;
+constexpr int kSvMaxCta = 8;
+
+__device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void widen(const uint4& w, float (&f)[4]) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+};
+template <>
+struct Piece<bf16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void widen(const uint4& w, float (&f)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+__device__ __forceinline__ float as_f(float x) { return x; }
+__device__ __forceinline__ float as_f(bf16 x) { return __bfloat162float(x); }
+
+// max(p - q, 0); a NaN or infinite probability counts as nothing.
+__device__ __forceinline__ double residual(float p, float q) {
+  return (p > q && p < INFINITY) ? static_cast<double>(p) - static_cast<double>(q) : 0.0;
+}
+
+// N consecutive probabilities at v (fewer at the row's end: the rest 0).
+template <typename T, bool kVec, int N>
+__device__ __forceinline__ void load_piece(const T* row, int v, int hi, float (&f)[N]) {
+  if constexpr (kVec) {
+    if (v < hi) {  // rows are a whole number of pieces
+      Piece<T>::widen(*reinterpret_cast<const uint4*>(row + v), f);
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = v + e < hi ? as_f(row[v + e]) : 0.f;
+}
+}  // namespace
+
+// kVec: rows and bases 16-byte aligned, 16-byte pieces; else one element a
+// lane (coalesced all the same).
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kSvThreads) spec_sample_kernel(const SpecSampleArgs a) {
+  constexpr int N = kVec ? Piece<T>::n : 1;
+  constexpr int kStep = 32 * N;
+  __shared__ double w_tot[kSvWarps];
+  __shared__ double c_tot[kSvMaxCta];
+  __shared__ int s_k;
+  const int n_cta = gridDim.x, rank = blockIdx.x, seq = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int K = a.K, V = a.V;
+  const T* tp = static_cast<const T*>(a.target_p) + static_cast<size_t>(seq) * (K + 1) * V;
+  const T* dp = a.draft_p ? static_cast<const T*>(a.draft_p) + static_cast<size_t>(seq) * K * V : nullptr;
+  const int32_t* ids = a.draft_ids + static_cast<size_t>(seq) * K;
+  cluster_arrive();  // every CTA of the cluster runs before any sends into it (the wait sits before the sends)
+
+  int nd = a.n_draft ? a.n_draft[seq] : K;
+  if (nd < 0 || nd > K) {
+    if (threadIdx.x == 0) record_error(a.status, DVLM_ERR_BOUNDS);
+    nd = nd < 0 ? 0 : K;
+  }
+  // every CTA of the cluster takes the K decisions for itself
+  if (warp == 0) {
+    int k = nd;
+    for (int j0 = 0; j0 < nd; j0 += 32) {
+      const int j = j0 + lane;
+      bool ok = true;
+      if (j < nd) {
+        const int x = ids[j];
+        ok = x >= 0 && x < V;
+        if (ok) {
+          const size_t at = static_cast<size_t>(j) * V + x;
+          const double q = dp ? static_cast<double>(as_f(dp[at])) : 1.0;
+          ok = static_cast<double>(a.u_accept[static_cast<size_t>(seq) * K + j]) * q <
+               static_cast<double>(as_f(tp[at]));
+        } else if (rank == 0) {
+          record_error(a.status, DVLM_ERR_BOUNDS);
+        }
+      }
+      const unsigned rej = __ballot_sync(0xffffffffu, !ok);
+      if (rej) {
+        k = j0 + __ffs(rej) - 1;
+        break;
+      }
+    }
+    if (lane == 0) s_k = k;
+  }
+  __syncthreads();
+  const int k = s_k;
+  const T* p = tp + static_cast<size_t>(k) * V;
+  const T* q = (dp && k < nd) ? dp + static_cast<size_t>(k) * V : nullptr;
+  int hot = (!dp && k < nd) ? ids[k] : -1;  // a draft without probabilities: q is 1 at its token
+
+  // warp stretches: whole steps, dealt in order over the cluster's warps
+  const int n_warp = n_cta * kSvWarps;
+  const int steps = (V + kStep - 1) / kStep, per = (steps + n_warp - 1) / n_warp;
+  const long long lo_l = static_cast<long long>(rank * kSvWarps + warp) * per * kStep;
+  const int lo = static_cast<int>(lo_l < V ? lo_l : V);
+  const int hi = static_cast<int>(lo_l + static_cast<long long>(per) * kStep < V ? lo_l + static_cast<long long>(per) * kStep : V);
+
+  auto values = [&](int v, double (&r)[N]) {
+    float fp[N], fq[N];
+    load_piece<T, kVec, N>(p, v, hi, fp);
+    if (q) {
+      load_piece<T, kVec, N>(q, v, hi, fq);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) fq[e] = v + e == hot ? 1.f : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) r[e] = residual(fp[e], fq[e]);
+  };
+
+  // u in [0, 1): anything else counts as the nearest value inside, so that a step is always found
+  float uf = a.u_sample[seq];
+  uf = uf >= 0.f ? fminf(uf, 0x1.fffffep-1f) : 0.f;
+  const double u = static_cast<double>(uf);
+  for (int pass = 0;; ++pass) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int v = lo + lane * N; v < hi; v += kStep) {
+      double r[N];
+      values(v, r);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum += r[e];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) w_tot[warp] = sum;
+    __syncthreads();
+    double mine = 0.0, before = 0.0;  // this CTA's total, and the warps before this one, in warp order
+#pragma unroll
+    for (int w = 0; w < kSvWarps; ++w) {
+      if (w == warp) before = mine;
+      mine += w_tot[w];
+    }
+    if (pass == 0) cluster_wait();
+    if (threadIdx.x < n_cta) st_dsmem_f64(map_to_cta(smem_u32(&c_tot[rank]), threadIdx.x), mine);
+    cluster_sync();
+    double total = 0.0, base = 0.0;
+    for (int c = 0; c < n_cta; ++c) {
+      if (c == rank) base = total;
+      total += c_tot[c];
+    }
+    if (total > 0.0) {
+      const double target = u * total;
+      // this warp's share (base + before, base + before + its sum], as every warp computes it
+      const double from = base + before, to = base + (before + w_tot[warp]);
+      if (from <= target && to > target) {
+        double run = from;
+        int found = -1, last = -1;
+        for (int v0 = lo; v0 < hi && found < 0; v0 += kStep) {
+          double r[N], c[N];
+          const int v = v0 + lane * N;
+          values(v, r);
+          c[0] = r[0];
+#pragma unroll
+          for (int e = 1; e < N; ++e) c[e] = c[e - 1] + r[e];
+          double inc = c[N - 1];
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+          }
+          const double ex = inc - c[N - 1];
+          int hit = 0x7fffffff, pos = -1;
+#pragma unroll
+          for (int e = N - 1; e >= 0; --e) {
+            if (r[e] > 0.0 && run + (ex + c[e]) > target) hit = v + e;
+            if (r[e] > 0.0 && pos < 0) pos = v + e;
+          }
+          hit = __reduce_min_sync(0xffffffffu, hit);
+          pos = __reduce_max_sync(0xffffffffu, pos);
+          if (pos >= 0) last = pos;
+          if (hit != 0x7fffffff) found = hit;
+          run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        // rounding in the walk may leave the step just past its end: the last
+        // token of the stretch that has any probability
+        if (lane == 0) a.out_ids[static_cast<size_t>(seq) * (K + 1) + k] = found >= 0 ? found : last;
+      }
+      break;
+    }
+    // nothing left of the residual: the target's own row; nothing there
+    // either is an error
+    if (pass == 1) {
+      if (rank == 0 && threadIdx.x == 0) {
+        record_error(a.status, DVLM_ERR_BOUNDS);
+        a.out_ids[static_cast<size_t>(seq) * (K + 1) + k] = 0;
+      }
+      break;
+    }
+    q = nullptr;
+    hot = -1;
+    cluster_sync();  // c_tot and w_tot have been read
+  }
+  if (rank == 0) {
+    for (int j = threadIdx.x; j <= K; j += kSvThreads)
+      if (j != k) a.out_ids[static_cast<size_t>(seq) * (K + 1) + j] = j < k ? ids[j] : -1;
+    if (threadIdx.x == 0) {
+      a.accept_len[seq] = k;
+      if (a.cache_len_out) a.cache_len_out[seq] = a.cache_len[seq] - (nd - k);
+    }
+  }
+}
+
+cudaError_t launch_spec_sample(const SpecSampleArgs& a, bool is_bf16, cudaStream_t s) {
+  const int es = is_bf16 ? 2 : 4;
+  const bool vec = (static_cast<long long>(a.V) * es) % 16 == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.target_p) & 15u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.draft_p) & 15u) == 0;
+  // CTAs per sequence: the portable cluster size, fewer for vocabularies that
+  // leave its warps without a step
+  const int steps = (a.V + 1023) / 1024;
+  int n_cta = 1;
+  while (n_cta < kSvMaxCta && n_cta * kSvWarps / 4 < steps) n_cta *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(n_cta, a.b);
+  cfg.blockDim = dim3(kSvThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = n_cta;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (is_bf16)
+    return vec ? cudaLaunchKernelEx(&cfg, spec_sample_kernel<bf16, true>, a)
+               : cudaLaunchKernelEx(&cfg, spec_sample_kernel<bf16, false>, a);
+  return vec ? cudaLaunchKernelEx(&cfg, spec_sample_kernel<float, true>, a)
+             : cudaLaunchKernelEx(&cfg, spec_sample_kernel<float, false>, a);
+}
+
+}  // namespace dvlm

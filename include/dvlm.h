@@ -271,6 +271,112 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
                                     dvlm_stream stream);
 
 /* ------------------------------------------------------------------------
+ * One batched step over paged KV caches: the requests' lengths become block
+ * tables and a slot map (dvlm_page_plan), the projected rows become rotated
+ * queries and cached keys and values (dvlm_mrope_append_paged), every request's
+ * rows attend to its pages (dvlm_chunk_attn_paged), and drafted tokens are
+ * verified against the target's probabilities (dvlm_spec_verify_sample).  The
+ * page stores, block tables and lengths are those of dvlm_block_attn_paged
+ * [Fast-dVLM technical overview (ocdem.com), section 2.3.2: paged KV cache
+ * management].  The rows of all requests of a step are packed one request
+ * behind the other: request b owns rows cu_rows[b] .. cu_rows[b + 1] - 1.
+ *
+ * Page plan of a ragged step.  cache_len [n_batch]: slots each request holds;
+ * new_len [n_batch]: rows it adds (0: idle; -1: finished, its pages go back);
+ * block_table [n_batch, max_pages] (in/out): the first ceil(cache_len / 64)
+ * entries of each row are its pages; free_pages [n_pages] (in/out) with
+ * free_count [1]: the stack of free pages, top at free_count - 1.  In this
+ * order: the pages of finished requests are pushed (request by request, page by
+ * page); then each request in turn takes the pages its new rows need from the
+ * top into its next table entries.  A request that finds too few pages, or
+ * whose rows would pass max_rows, waits, and so does every request behind it:
+ * it adds no rows this step (DVLM_ERR_CACHE_OVERFLOW in *dev_status if it
+ * wanted any).  Outputs: kv_len [n_batch] (slots after the step; 0 for a
+ * finished request), cu_rows [n_batch + 1], slot_map [max_rows] (page * 64 +
+ * row in page of every row; -1 behind the last request's rows),
+ * free_count_out [1].  kv_len may be cache_len and free_count_out may be
+ * free_count; no other arrays may overlap.  A request whose cached length is
+ * outside 0 .. 64 max_pages, whose new length is below -1, or whose sum is
+ * past 64 max_pages takes no part (kv_len: 0 in the first two cases, its
+ * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
+ * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
+ * numbers are passed on as they are.  All pointers device int32.  n_batch <=
+ * 4096, n_pages and max_pages < 2^25.  Errors: INVALID_ARG, SHAPE.  One
+ * launch, no workspace. */
+DVLM_API dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
+                                   int32_t* free_pages, const int32_t* free_count, int n_batch, int max_pages,
+                                   int n_pages, int max_rows, int32_t* kv_len, int32_t* cu_rows,
+                                   int32_t* slot_map, int32_t* free_count_out, int* dev_status,
+                                   dvlm_stream stream);
+
+/* Rotary positions with several axes (rows of images and video have a time, a
+ * height and a width position; text rows the same value on every axis).  The
+ * first rot_dim elements of each head turn in pairs (j, j + rot_dim / 2) by
+ * pos[axis(j)][row] * rope_base^(-2j / rot_dim); the rest passes unchanged.
+ * pos [n_axes, n_rows]: device int32, any sign.  sections (HOST int [n_axes],
+ * sum rot_dim / 2): how many frequencies each axis takes -- in order, axis 0's
+ * first (interleaved = 0), or interleaved = 1: frequency j goes to axis j %
+ * n_axes while j < n_axes * sections of that axis, else to axis 0.  Angles are
+ * reduced in fp64; products in fp32; one rounding to the output.  With one
+ * axis and rot_dim = D this is the model's own rotate-half RoPE.
+ * x, out: n_rows rows of n_heads heads of D, row strides x_ld, out_ld
+ * (elements); out may be x (same stride), else they must not overlap.
+ * DVLM_BF16 or DVLM_FP32.  1 <= n_axes <= 4, D <= 256, n_heads * D <= 2^24.
+ * Errors: INVALID_ARG (null or misaligned pointer, type, interleaved not 0 or
+ * 1, rope_base not positive), SHAPE.  dev_status is unused. */
+DVLM_API dvlm_status dvlm_mrope(const void* x, void* out, const int32_t* pos, int n_rows, int n_heads, int D,
+                               long long x_ld, long long out_ld, int rot_dim, int n_axes, const int* sections,
+                               float rope_base, int interleaved, dvlm_dtype dt, int* dev_status,
+                               dvlm_stream stream);
+
+/* dvlm_mrope on the query and key heads of projected rows, with the split of
+ * the rows and the write of the new keys and values into their pages.  qkv
+ * [n_rows, >= (Hq + 2 Hkv) D] (row stride qkv_ld elements, a multiple of 8):
+ * Hq query heads, Hkv key heads, Hkv value heads; q_out [n_rows, Hq, D];
+ * k_pages [n_pages, Hkv, 64, D], v_pages [n_pages, Hkv, D, 64] (transposed);
+ * all bf16, 16-byte aligned.  slot_map [n_rows] (device int32, of
+ * dvlm_page_plan): row r's key and value go to row slot % 64 of page slot /
+ * 64.  A row with slot -1 is padding: nothing of it is written, its row of
+ * q_out included.  Any other slot outside the pages sets DVLM_ERR_BOUNDS and
+ * is skipped the same way.  Two rows with the same slot leave either row's
+ * values there.  D == 64 or 128.  Errors as dvlm_mrope, UNSUPPORTED for other
+ * head sizes. */
+DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos, const int32_t* slot_map,
+                                            void* q_out, void* k_pages, void* v_pages, int n_rows, int Hq, int Hkv,
+                                            int D, int n_pages, long long qkv_ld, int rot_dim, int n_axes,
+                                            const int* sections, float rope_base, int interleaved,
+                                            int* dev_status, dvlm_stream stream);
+
+/* Verification of drafted tokens against the target's probabilities from given
+ * random numbers (the sampled counterpart of dvlm_spec_verify_accept: accepted
+ * and drawn tokens together follow the target's distribution).  Per sequence
+ * i: draft j < n_draft[i] with token x is accepted while u_accept[i, j] *
+ * draft_p[i, j, x] < target_p[i, j, x]; k = accept_len[i] drafts are accepted.
+ * Then one token is drawn: the lowest v whose cumulative sum of r[0..v] passes
+ * u_sample[i] times the whole sum, where r = max(target_p[i, k] - draft_p[i,
+ * k], 0) if a draft was refused, and r = target_p[i, n_draft[i]] if all were
+ * accepted.  out_ids[i] = the k accepted drafts, the drawn token, then -1.
+ * target_p [b, K + 1, V], draft_p [b, K, V] (fp32 or bf16; draft_p NULL: each
+ * draft has probability 1 on its token, as a drafted argmax has); draft_ids
+ * [b, K] int32; u_accept [b, K], u_sample [b] fp32 in [0, 1); n_draft [b] int32
+ * (NULL: K everywhere; rows past it are not read); accept_len [b], out_ids
+ * [b, K + 1] int32.  When cache_len (device int32 [b], slots after the
+ * verify pass wrote the n_draft rows) and cache_len_out are given, the latter
+ * receives cache_len - (n_draft - k): the cache cut back to the accepted rows;
+ * it may be the same array.  Rows need not sum to 1.  NaN and infinite
+ * probabilities count as 0 in a draw and refuse a draft.  u_sample outside
+ * [0, 1) counts as the nearest value inside.  If r is 0 everywhere the draw is
+ * from the target row itself; if that is 0 too, token 0 and DVLM_ERR_BOUNDS.
+ * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS), as is an n_draft
+ * outside 0..K (cut to it).  1 <= K <= 64, b <= 65535, V <= 2^30.  Sums and
+ * decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace. */
+DVLM_API dvlm_status dvlm_spec_verify_sample(const void* target_p, const void* draft_p, const int32_t* draft_ids,
+                                            const int32_t* n_draft, const float* u_accept, const float* u_sample,
+                                            int b, int K, int V, dvlm_dtype dt, int32_t* accept_len,
+                                            int32_t* out_ids, const int32_t* cache_len, int32_t* cache_len_out,
+                                            int* dev_status, dvlm_stream stream);
+
+/* ------------------------------------------------------------------------
  * Decoder model and decode engine.
  *
  * dvlm_model holds non-owning views of device weights, all [out, in]

@@ -164,3 +164,98 @@ def test_binding_declares_every_header_entry_point():
     import re
     src = inspect.getsource(binding._declare)
     assert set(re.findall(r'"(dvlm_\w+)"', src)) == set(dv.declared_symbols())
+
+
+def _plan(**kw):
+    a = dict(cache=16, new=16, table=16, free=16, count=16, n=4, mp=8, np=32, rows=64, kv=16, cu=16, slots=16, out=16)
+    a.update(kw)
+    return dv.lib().dvlm_page_plan(a["cache"], a["new"], a["table"], a["free"], a["count"], a["n"], a["mp"], a["np"],
+                                   a["rows"], a["kv"], a["cu"], a["slots"], a["out"], None, None)
+
+
+def test_page_plan_host_validation(dvlm_lib):
+    for name in ("cache", "new", "table", "free", "count", "kv", "cu", "slots", "out"):
+        assert _plan(**{name: None}) == INVALID
+    for kw in (dict(n=0), dict(n=4097), dict(mp=0), dict(mp=1 << 25), dict(np=0), dict(np=1 << 25), dict(rows=0)):
+        assert _plan(**kw) == SHAPE
+
+
+def _mrope(**kw):
+    a = dict(x=16, out=32, pos=16, rows=4, heads=2, D=64, x_ld=128, o_ld=128, rot=64, n=3, sec=(12, 10, 10), base=1e4,
+             il=0, dt=0)
+    a.update(kw)
+    sec = (ctypes.c_int * len(a["sec"]))(*a["sec"]) if a["sec"] is not None else None
+    return dv.lib().dvlm_mrope(a["x"], a["out"], a["pos"], a["rows"], a["heads"], a["D"], a["x_ld"], a["o_ld"],
+                               a["rot"], a["n"], sec, a["base"], a["il"], a["dt"], None, None)
+
+
+def _append(**kw):
+    a = dict(qkv=16, pos=16, slots=16, q=16, k=16, v=16, rows=4, Hq=2, Hkv=1, D=64, np=4, ld=256, rot=64, n=3,
+             sec=(12, 10, 10), base=1e4, il=0)
+    a.update(kw)
+    sec = (ctypes.c_int * len(a["sec"]))(*a["sec"]) if a["sec"] is not None else None
+    return dv.lib().dvlm_mrope_append_paged(a["qkv"], a["pos"], a["slots"], a["q"], a["k"], a["v"], a["rows"], a["Hq"],
+                                            a["Hkv"], a["D"], a["np"], a["ld"], a["rot"], a["n"], sec, a["base"],
+                                            a["il"], None, None)
+
+
+def test_mrope_host_validation(dvlm_lib):
+    for f in (_mrope, _append):
+        assert f(pos=None) == INVALID and f(sec=None) == INVALID
+        assert f(il=2) == INVALID and f(base=0.0) == INVALID and f(base=float("nan")) == INVALID
+        assert f(n=0) == SHAPE and f(n=5, sec=(12, 10, 10, 0, 0)) == SHAPE
+        assert f(sec=(12, 10, 11)) == SHAPE and f(sec=(42, -10, 0)) == SHAPE
+        assert f(rot=63) == SHAPE and f(rot=66, sec=(13, 10, 10)) == SHAPE and f(rot=0, sec=(0, 0, 0)) == SHAPE
+        assert f(rows=0) == SHAPE
+    assert _mrope(x=None) == INVALID and _mrope(out=None) == INVALID and _mrope(dt=2) == INVALID
+    assert _mrope(x=17) == INVALID and _mrope(dt=1, x=18) == INVALID
+    assert _mrope(D=258, x_ld=1000, o_ld=1000) == SHAPE and _mrope(x_ld=127) == SHAPE and _mrope(o_ld=127) == SHAPE
+    assert _mrope(out=16, o_ld=136) == SHAPE and _mrope(heads=0) == SHAPE
+    for name in ("qkv", "slots", "q", "k", "v"):
+        assert _append(**{name: None}) == INVALID
+    for name in ("qkv", "q", "k", "v"):
+        assert _append(**{name: 24}) == INVALID
+    assert _append(D=80, rot=64, ld=400) == UNSUPPORTED
+    assert _append(ld=248) == SHAPE and _append(ld=260) == SHAPE
+    assert _append(np=0) == SHAPE and _append(np=1 << 25) == SHAPE and _append(Hkv=0) == SHAPE
+
+
+def _verify(**kw):
+    a = dict(p=16, q=16, ids=16, nd=None, u=16, us=16, b=1, K=4, V=100, dt=0, acc=16, out=16, cl=None, co=None)
+    a.update(kw)
+    return dv.lib().dvlm_spec_verify_sample(a["p"], a["q"], a["ids"], a["nd"], a["u"], a["us"], a["b"], a["K"], a["V"],
+                                            a["dt"], a["acc"], a["out"], a["cl"], a["co"], None, None)
+
+
+def test_verify_sample_host_validation(dvlm_lib):
+    for name in ("p", "ids", "u", "us", "acc", "out"):
+        assert _verify(**{name: None}) == INVALID
+    assert _verify(cl=16) == INVALID and _verify(co=16) == INVALID
+    assert _verify(dt=2) == INVALID and _verify(p=17) == INVALID and _verify(dt=1, q=18) == INVALID
+    for kw in (dict(b=0), dict(b=65536), dict(K=0), dict(K=65), dict(V=0), dict(V=(1 << 30) + 1)):
+        assert _verify(**kw) == SHAPE
+
+
+def test_step_binding_refuses_what_it_would_misread(dvlm_lib):
+    """Wrong types, sizes and devices raise before the library is called."""
+    import pytest
+    import torch
+    i = torch.zeros(8, dtype=torch.int32)
+    kw = dict(n_batch=4, max_pages=2, n_pages=8, max_rows=8, kv_len=i, cu_rows=i, slot_map=i, free_count_out=i)
+    with pytest.raises(dv.DvlmError):
+        dv.page_plan(i.long(), i, i, i, i, **kw)
+    with pytest.raises(dv.DvlmError):
+        dv.page_plan(i, i, i[:7], i, i, **kw)
+    with pytest.raises(dv.DvlmError):
+        dv.page_plan(i, i, i, i, i, **kw)               # host tensors
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    mk = dict(n_rows=4, n_heads=2, D=64, sections=(32,), rope_base=1e4, dtype=dv.DVLM_BF16)
+    for bad in (x.float(), x[:, :1], x[:3], x.transpose(0, 1)):
+        with pytest.raises(dv.DvlmError):
+            dv.mrope(bad, x, i, **mk)
+    p = torch.zeros(1, 5, 100)
+    vk = dict(b=1, K=4, V=100, dtype=dv.DVLM_FP32, accept_len=i, out_ids=i)
+    u = torch.zeros(4)
+    for args in ((p.bfloat16(), None, i, u, u), (p[:, :4], None, i, u, u), (p, p[:, :3], i, u, u), (p, None, i, u.double(), u)):
+        with pytest.raises(dv.DvlmError):
+            dv.spec_verify_sample(*args, **vk)
