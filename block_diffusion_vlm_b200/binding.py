@@ -131,6 +131,8 @@ def _declare(L: ctypes.CDLL) -> None:
         "dvlm_page_plan": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 6),
         "dvlm_mrope": (_i, [_vp, _vp, _vp, _i, _i, _i, _ll, _ll, _i, _i, _vp, _f, _i, _i, _vp, _vp]),
         "dvlm_mrope_append_paged": (_i, [_vp] * 6 + [_i] * 5 + [_ll, _i, _i, _vp, _f, _i, _vp, _vp]),
+        "dvlm_chunk_attn_paged_workspace_size": (_sz, [_i] * 5),
+        "dvlm_chunk_attn_paged": (_i, [_vp] * 10 + [_i] * 7 + [_ll, _f, _vp, _sz, _vp, _vp]),
         "dvlm_spec_verify_sample": (_i, [_vp] * 6 + [_i] * 4 + [_vp] * 6),
     }
     for name, (res, args) in sigs.items():
@@ -356,6 +358,27 @@ def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, H
     _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, ptr(qkv), ptr(pos), ptr(slot_map),
             ptr(q_out), ptr(k_pages), ptr(v_pages), n_rows, Hq, Hkv, D, n_pages, qkv_ld, rot_dim or D, len(sec), sec,
             float(rope_base), int(interleaved), ptr(status))
+
+
+def chunk_attn_paged_workspace_size(n_batch: int, n_rows: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().dvlm_chunk_attn_paged_workspace_size(n_batch, n_rows, Hq, Hkv, D))
+
+
+def chunk_attn_paged(q, out, k_pages, v_pages, block_table, kv_len, cu_rows, *, n_batch, n_rows, n_pages, max_pages,
+                     Hq, Hkv, D, scale, workspace, n_noisy=None, n_hidden=None, lse=None, q_ld=0, status=None,
+                     stream=None) -> None:
+    """Attention of ragged chunks of rows over paged caches (dvlm_chunk_attn_paged)."""
+    import torch
+    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
+    q_ld = _rows("dvlm_chunk_attn_paged", q, bf, n_rows, q_ld, Hq * D, dev)
+    _take("dvlm_chunk_attn_paged", dev, (out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
+          (v_pages, bf, n_pages * Hkv * 64 * D), (block_table, i32, n_batch * max_pages), (kv_len, i32, n_batch),
+          (cu_rows, i32, n_batch + 1), (n_noisy, i32, n_batch), (n_hidden, i32, n_batch),
+          (lse, torch.float32, n_rows * Hq), (status, i32, 1))
+    _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, ptr(q), ptr(out), ptr(k_pages),
+            ptr(v_pages), ptr(block_table), ptr(kv_len), ptr(cu_rows), ptr(n_noisy), ptr(n_hidden), ptr(lse), n_batch,
+            n_rows, n_pages, max_pages, Hq, Hkv, D, q_ld, float(scale), ptr(workspace),
+            workspace.numel() * workspace.element_size(), ptr(status))
 
 
 def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K, V, dtype, accept_len, out_ids,

@@ -484,6 +484,58 @@ dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos, const i
   return cuda_status(launch_mrope_append(a, D, cs(stream)));
 }
 
+size_t dvlm_chunk_attn_paged_workspace_size(int n_batch, int n_rows, int Hq, int Hkv, int D) {
+  if (n_batch < 1 || n_rows < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
+  return attn_chunk_scratch_bytes(sms_or_default(), D);
+}
+
+dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void* k_pages, const void* v_pages,
+                                  const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_rows,
+                                  const int32_t* n_noisy, const int32_t* n_hidden, float* lse, int n_batch,
+                                  int n_rows, int n_pages, int max_pages, int Hq, int Hkv, int D, long long q_ld,
+                                  float scale, void* workspace, size_t ws_bytes, int* dev_status,
+                                  dvlm_stream stream) {
+  if (!q || !out || !k_pages || !v_pages || !block_table || !kv_len || !cu_rows) return DVLM_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return DVLM_ERR_INVALID_ARG;
+  if (n_batch < 1 || n_rows < 1 || n_pages < 1 || n_pages > kMaxPages || max_pages < 1 || max_pages > kMaxPages ||
+      Hq < 1 || Hkv < 1 || Hq > 4096 || D < 1 || Hq % Hkv)
+    return DVLM_ERR_SHAPE;
+  // page rows are TMA coordinates: n_pages * Hkv * max(64, D) stays in 31 bits
+  if (static_cast<long long>(n_pages) * Hkv * (D > 64 ? D : 64) > 0x7fffffffLL) return DVLM_ERR_SHAPE;
+  if (q_ld < static_cast<long long>(Hq) * D || q_ld % 8) return DVLM_ERR_SHAPE;
+  const int G = Hq / Hkv;
+  if ((D != 64 && D != 128) || G > 128) return DVLM_ERR_UNSUPPORTED;
+  if (!al16(q) || !al16(out) || !al16(k_pages) || !al16(v_pages)) return DVLM_ERR_INVALID_ARG;
+  const int P = sms_or_default();
+  if (!workspace || ws_bytes < attn_chunk_scratch_bytes(P, D)) return DVLM_ERR_WORKSPACE;
+  if (!al16(workspace)) return DVLM_ERR_INVALID_ARG;
+  CUtensorMap mq, mk, mv;
+  const uint64_t page_rows = static_cast<uint64_t>(n_pages) * Hkv;
+  bool ok = make_tmap_3d(&mq, q, D, Hq, n_rows, static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(q_ld) * 2, 64, G,
+                         128 / G);
+  ok &= make_tmap_2d(&mk, k_pages, D, page_rows * 64, static_cast<uint64_t>(D) * 2, 64, 64);
+  ok &= make_tmap_2d(&mv, v_pages, 64, page_rows * D, 64 * 2, 64, D);
+  if (!ok) return DVLM_ERR_CUDA;
+  ChunkAttnArgs a{};
+  a.out = static_cast<bf16*>(out);
+  a.lse = lse;
+  a.block_table = block_table;
+  a.kv_len = kv_len;
+  a.cu_rows = cu_rows;
+  a.n_noisy = n_noisy;
+  a.n_hidden = n_hidden;
+  a.n_batch = n_batch;
+  a.n_rows = n_rows;
+  a.n_pages = n_pages;
+  a.max_pages = max_pages;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  a.workspace = workspace;
+  a.status = dev_status;
+  return cuda_status(launch_attn_chunk(mq, mk, mv, a, D, P, cs(stream)));
+}
+
 dvlm_status dvlm_spec_verify_sample(const void* target_p, const void* draft_p, const int32_t* draft_ids,
                                     const int32_t* n_draft, const float* u_accept, const float* u_sample, int b, int K,
                                     int V, dvlm_dtype dt, int32_t* accept_len, int32_t* out_ids,

@@ -1,0 +1,870 @@
+// Attention of ragged chunks of new rows over paged K/V caches, bf16, tcgen05.
+//
+// Mathematics: row t of request b (n new rows behind kv - n cached slots) sees
+// slots hidden .. kv - n + t, or hidden .. kv - 1 for the request's last
+// `noisy` rows; o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) over the
+// visible slots j, s = scale q.k, with the running maximum and sum of an
+// online softmax; a row that sees nothing gives 0.  Partial results over
+// disjoint slots combine by their (m, l): o = sum_i e^(m_i - m) o_i / sum_i
+// e^(m_i - m) l_i.
+//
+// Tile: the G = Hq / Hkv query heads of a KV head times 128 / G rows fill the
+// 128 lanes of an MMA, so a single-token row of 8 heads costs the cache read
+// once, not 8 times.  A CTA works on two tiles at a time, each with its own
+// softmax warpgroup (a thread owns a row), S and P sharing TMEM columns and O
+// beside them (2 x 128 + 2 x D columns):
+//   pair: two neighbouring row tiles of one request and KV head over the same
+//         128-slot chunks (each K and V chunk is loaded once for 256 rows);
+//   solo: one row tile; the two warpgroups take alternate chunks and combine
+//         their (m, l, O) through TMEM at the end, so that few rows keep both
+//         halves of the SM busy.
+// The tensor pipe alternates between the tiles: while one tile's scores are
+// exponentiated, the other's P V and next Q K^T run.
+//
+// Work split: all (request, KV head, pair or solo item) are laid end to end by
+// their cost in slots, and the line is cut into equal parts, one per CTA (one
+// CTA per SM).  A cut inside an item leaves partial (O, m, l) in the workspace
+// (at most two per CTA) for the merge kernel; every other row is written
+// directly.  The cost of a request's items is a closed form (chunk ends grow
+// linearly), so each CTA finds its part from the lengths on the device alone:
+// no host knowledge of them, no plan kernel.
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dvlm {
+
+namespace {
+constexpr int kAcThreads = 320;  // warp 0 loads and schedules, 1 issues MMAs, 2..5 and 6..9 softmax
+constexpr int kAcKeys = 128;     // slots per chunk: two pages
+constexpr int kAcRing = 4;       // work descriptors in flight
+constexpr int kAcItemCost = 256; // fixed cost of an item, in slot units (prologue and epilogue)
+constexpr int kAcMinPart = 384;  // least cost worth a CTA of its own
+constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
+
+template <int D>
+struct AcCfg {
+  static constexpr int kStage = kAcKeys * D * 2;  // one K or V^T chunk
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kQ = 128 * D * 2;          // one Q tile
+  static constexpr int oQ = 0;
+  static constexpr int oKV = 2 * kQ;
+  static constexpr int oBar = oKV + kStages * kStage;
+  static constexpr int kBars = 2 * kAcRing + 2 + 2 * kStages + 7;
+  static constexpr int oDesc = oBar + 512;
+  static constexpr int oML = oDesc + kAcRing * 64;
+  static constexpr int kSmem = oML + 2 * 128 * 8 + 1024;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kAcKeys);
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(128, D);
+};
+constexpr uint32_t kAcColO = 256;
+
+// One request's lengths and the closed form of its items' costs.
+struct Req {
+  int row0, n, kv, nclean, hid, base;
+  int pairs, solo, pc;  // pair items, solo items (0 or 1), leading pairs that are whole and causal
+};
+
+__device__ __forceinline__ Req load_req(const ChunkAttnArgs& a, int b, int tpt, int* err) {
+  Req r;
+  int lo = a.cu_rows[b], hi = a.cu_rows[b + 1], kv = a.kv_len[b];
+  if (lo < 0 || hi < lo || hi > a.n_rows || kv < 0 || kv > a.max_pages * 64LL || hi - lo > kv) {
+    *err = 1;  // takes no part
+    lo = hi = kv = 0;
+  }
+  r.row0 = lo;
+  r.n = hi - lo;
+  r.kv = kv;
+  r.base = kv - r.n;
+  int noisy = a.n_noisy ? a.n_noisy[b] : 0;
+  int hid = a.n_hidden ? a.n_hidden[b] : 0;
+  r.nclean = r.n - max(0, min(noisy, r.n));
+  r.hid = max(0, min(hid, kv));
+  const int tiles = (r.n + tpt - 1) / tpt;
+  r.pairs = tiles >> 1;
+  r.solo = tiles & 1;
+  r.pc = min(r.pairs, r.nclean / (2 * tpt));
+  return r;
+}
+// Cost of the first i pair items of a request: sum of 2 * (visible slots) +
+// kAcItemCost, the slots counted from the hidden prefix's chunk on.
+__device__ __forceinline__ long long pair_prefix(const Req& r, int tpt, int i) {
+  const long long p2 = 2 * tpt, off = r.base - (r.hid & ~(kAcKeys - 1));
+  const long long k = min(i, r.pc);
+  long long k0 = off < 0 ? min(k, -off / p2) : 0;  // leading items that end at or before the first visible chunk
+  long long c = (k - k0) * off + p2 * (k * (k + 1) / 2 - k0 * (k0 + 1) / 2);
+  c += (i - k) * max(0LL, static_cast<long long>(r.kv) - (r.hid & ~(kAcKeys - 1)));
+  return 2 * c + static_cast<long long>(i) * kAcItemCost;
+}
+__device__ __forceinline__ long long solo_cost(const Req& r) {
+  return max(0, r.kv - (r.hid & ~(kAcKeys - 1))) + kAcItemCost;
+}
+__device__ __forceinline__ long long req_cost(const Req& r, int tpt) {
+  return pair_prefix(r, tpt, r.pairs) + (r.solo ? solo_cost(r) : 0);
+}
+
+// Work descriptor (16 ints in shared memory).
+struct Work {
+  int kind;             // 0 end, 1 pair, 2 solo
+  int c0, nc;           // first chunk, chunks
+  int row0, ntok;       // first row (of all rows) and rows of the item
+  int t0;               // the item's first row within the request
+  int nclean, base, kv, hid;
+  int g;                // KV head
+  int slot;             // -1: whole item; 0 / 1: partial, this CTA's slot
+  int b;
+  int pad[3];
+};
+static_assert(sizeof(Work) == 64, "descriptor size");
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Wait for this thread's TMEM loads; the registers pass through so that no
+// use of them moves above the wait.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) { return ex2_approx(x); }
+}  // namespace
+
+// Partial results in the workspace: per CTA two slots of two tiles, O [D][128]
+// fp32 (feature-major: a warp stores 32 rows of a feature at once) and (m, l)
+// [128]; then one merge record per CTA.
+struct AcPart {
+  float* o;       // [P][2][2][D][128]
+  float2* ml;     // [P][2][2][128]
+  int* rec;       // [P][16]
+};
+static __host__ __device__ AcPart ac_carve(void* ws, int P, int D) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  AcPart a;
+  a.o = reinterpret_cast<float*>(p);
+  p += static_cast<size_t>(P) * 4 * D * 128 * 4;
+  a.ml = reinterpret_cast<float2*>(p);
+  p += static_cast<size_t>(P) * 4 * 128 * 8;
+  a.rec = reinterpret_cast<int*>(p);
+  return a;
+}
+size_t attn_chunk_scratch_bytes(int P, int D) {
+  return static_cast<size_t>(P) * 4 * D * 128 * 4 + static_cast<size_t>(P) * 4 * 128 * 8 + static_cast<size_t>(P) * 64;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAcThreads, 1)
+    attn_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                      const __grid_constant__ CUtensorMap mapV, const ChunkAttnArgs a) {
+  using C = AcCfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem + C::oQ;
+  uint8_t* sKV = smem + C::oKV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::oBar);
+  uint64_t* d_full = bars;                 // [kAcRing] descriptor written
+  uint64_t* d_empty = d_full + kAcRing;    // [kAcRing] MMA and softmax warps done with it
+  uint64_t* q_full = d_empty + kAcRing;
+  uint64_t* q_empty = q_full + 1;          // every S of the item done
+  uint64_t* kv_full = q_empty + 1;         // [NS]
+  uint64_t* kv_empty = kv_full + NS;       // [NS]
+  uint64_t* s_full = kv_empty + NS;        // [2] scores of a chunk (and all earlier products) done
+  uint64_t* p_full = s_full + 2;           // [2] P written, O rescaled
+  uint64_t* o_done = p_full + 2;           // [2] last P V of the item done
+  uint64_t* x_bar = o_done + 2;            // the softmax warps of both tiles meet (a bounded wait, unlike bar.sync)
+  static_assert(C::kBars * 8 + 16 <= 512, "barrier space");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* sabort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Work* desc = reinterpret_cast<Work*>(smem + C::oDesc);
+  float2* sML = reinterpret_cast<float2*>(smem + C::oML);  // [2][128] solo: both warpgroups' (m, l)
+  __shared__ long long s_scan[kAcThreads / 32];
+  __shared__ long long s_find[2];  // (request, its first cost) holding this CTA's first unit
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int P = gridDim.x, cta = blockIdx.x;
+  const int G = a.Hq / a.Hkv, tpt = 128 / G;
+  const AcPart ws = ac_carve(a.workspace, P, D);
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      uint64_t* b = &bars[i];
+      mbar_init(b, (b >= d_empty && b < q_full) ? 9 : (b >= p_full && b < o_done) ? 4 : b == x_bar ? 8 : 1);
+    }
+    *sabort = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&mapQ);
+    tma_prefetch_map(&mapK);
+    tma_prefetch_map(&mapV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // ------------------------------------------------ this CTA's part of the line
+  const int per = (a.n_batch + kAcThreads - 1) / kAcThreads;
+  const int b0 = min(a.n_batch, tid * per), b1 = min(a.n_batch, b0 + per);
+  int bad = 0;
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += a.Hkv * req_cost(load_req(a, b, tpt, &bad), tpt);
+  if (bad && cta == 0) record_error(a.status, DVLM_ERR_BOUNDS);
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) s_scan[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAcThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total += s_scan[w];
+  }
+  const long long parts = max(1LL, min(static_cast<long long>(P), total / kAcMinPart));
+  const long long lo = cta < parts ? total * cta / parts : total;
+  const long long hi = cta < parts ? total * (cta + 1) / parts : total;
+  long long at = before + inc - mine;
+  if (lo < hi && at <= lo && lo < at + mine) {  // one thread's requests hold the first unit
+    for (int b = b0; b < b1; ++b) {
+      const long long c = a.Hkv * req_cost(load_req(a, b, tpt, &bad), tpt);
+      if (lo < at + c) {
+        s_find[0] = b;
+        s_find[1] = at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+
+  // whole warps wait as one: either every lane goes on or none does
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, sabort)) != 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------ schedule and load
+    const uint64_t pol = l2_policy_evict_last();
+    int it = 0;        // descriptors issued
+    int pos = 0;       // K/V ring position
+    int nq = 0;        // Q loads issued
+    bool ok = true;
+    int rec_kind = 0;  // this CTA's item that goes on in the next CTAs
+    Work rw{};
+    int rec_last = 0;
+    if (lo < hi) {
+      int b = static_cast<int>(s_find[0]);
+      long long start = s_find[1];  // cost position of the current item
+      Req r = load_req(a, b, tpt, &bad);
+      long long per_head = req_cost(r, tpt);
+      int g = static_cast<int>((lo - start) / per_head);
+      start += g * per_head;
+      int i = 0;
+      {  // last item whose prefix is at or below lo
+        int l = 0, h = r.pairs + r.solo;
+        while (h - l > 1) {
+          const int m = (l + h) >> 1;
+          if (start + pair_prefix(r, tpt, m) <= lo) l = m;
+          else h = m;
+        }
+        i = l;
+        start += pair_prefix(r, tpt, i);
+      }
+      long long x = lo;
+      while (x < hi && ok) {
+        const bool solo = i == r.pairs;
+        const long long w = solo ? solo_cost(r) : pair_prefix(r, tpt, i + 1) - pair_prefix(r, tpt, i);
+        const long long xa = x - start, xb = min(w, hi - start);
+        Work k{};
+        k.kind = solo ? 2 : 1;
+        k.t0 = i * 2 * tpt;
+        k.ntok = min(2 * tpt, r.n - k.t0);
+        if (solo) k.ntok = r.n - k.t0;
+        k.row0 = r.row0 + k.t0;
+        k.nclean = r.nclean;
+        k.base = r.base;
+        k.kv = r.kv;
+        k.hid = r.hid;
+        k.g = g;
+        k.b = b;
+        const int te = k.t0 + k.ntok, end = te > r.nclean ? r.kv : r.base + te;
+        const int cb = r.hid / kAcKeys, nch = end > r.hid ? (end + kAcKeys - 1) / kAcKeys - cb : 0;
+        // cut positions in chunks; a solo item is cut in pairs of chunks
+        const int unit = solo ? 2 : 1;
+        const long long nu = (nch + unit - 1) / unit;
+        const int ca = static_cast<int>(nu * xa / w) * unit;
+        const int ce = xb == w ? nch : static_cast<int>(nu * xb / w) * unit;
+        k.c0 = cb + ca;
+        k.nc = max(0, min(ce, nch) - ca);
+        k.slot = (xa == 0 && xb == w) ? -1 : (xa == 0 ? 1 : 0);
+        if (k.slot == 1) {  // the item goes on: the CTA that holds its last unit
+          rec_kind = k.kind;
+          rw = k;
+          rec_last = static_cast<int>(((start + w) * parts - 1) / total);
+        }
+        // hand the descriptor over
+        const int slot = it % kAcRing;
+        if (it >= kAcRing) ok = warp_wait(&d_empty[slot], ((it / kAcRing) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          desc[slot] = k;
+          mbar_arrive(&d_full[slot]);
+        }
+        ++it;
+        if (k.nc > 0) {
+          // Q: rows [row0, +tpt) (and the next tpt for a pair) of the KV head's query heads
+          if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1);
+          if (!ok) break;
+          const int n_q = k.kind == 1 ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full, n_q * tpt * G * D * 2);
+            for (int w2 = 0; w2 < n_q; ++w2)
+              for (int d = 0; d < D / 64; ++d)
+                tma_load_3d(sQ + w2 * C::kQ + d * 16384, &mapQ, q_full, d * 64, g * G, k.row0 + w2 * tpt, pol);
+          }
+          ++nq;
+          // K and V in the order the products take them: K of the first chunk
+          // (two for a solo item), then V(c), K(c + lag)
+          const int lag = k.kind == 1 ? 1 : 2;
+          const int n_held = (r.kv + 63) >> 6;
+          int page_base = -1, page_v = 0;
+          auto page_of = [&](int p) -> int {  // logical page -> page number, 32 at a time
+            if (page_base < 0 || p < page_base || p >= page_base + 32) {
+              page_base = p;
+              page_v = 0;
+              if (p + lane < n_held) {
+                page_v = a.block_table[static_cast<size_t>(b) * a.max_pages + p + lane];
+                if (page_v < 0 || page_v >= a.n_pages) {
+                  record_error(a.status, DVLM_ERR_BOUNDS);
+                  page_v = 0;
+                }
+              }
+            }
+            return __shfl_sync(0xffffffffu, page_v, p - page_base);
+          };
+          // K runs ahead of V: one lookup window each would thrash, so a
+          // window starts at V's page and spans K's
+          auto load = [&](int c, bool is_v) {
+            const int st = pos % NS;
+            if (pos >= NS) ok = warp_wait(&kv_empty[st], ((pos / NS) - 1) & 1);
+            if (!ok) return;
+            const int p0 = 2 * (k.c0 + c), np = p0 + 1 < n_held ? 2 : 1;
+            const int pg0 = page_of(p0), pg1 = np == 2 ? page_of(p0 + 1) : 0;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&kv_full[st], np * 64 * D * 2);
+              uint8_t* dst = sKV + st * C::kStage;
+              for (int h = 0; h < np; ++h) {
+                const int entry = (h ? pg1 : pg0) * a.Hkv + g;
+                if (is_v) {
+                  tma_load_2d(dst + h * (D * 128), &mapV, &kv_full[st], 0, entry * D, pol);
+                } else {
+                  for (int d = 0; d < D / 64; ++d)
+                    tma_load_2d(dst + d * 16384 + h * 8192, &mapK, &kv_full[st], d * 64, entry * 64, pol);
+                }
+              }
+            }
+            ++pos;
+          };
+          for (int c = 0; c < min(lag, k.nc) && ok; ++c) load(c, false);
+          for (int c = 0; c < k.nc && ok; ++c) {
+            load(c, true);
+            if (ok && c + lag < k.nc) load(c + lag, false);
+          }
+        }
+        // next item
+        x = start + xb;
+        if (x < hi) {
+          start += w;
+          if (++i >= r.pairs + r.solo) {
+            i = 0;
+            if (++g >= a.Hkv) {
+              g = 0;
+              do {
+                ++b;
+                r = load_req(a, b, tpt, &bad);
+              } while (r.n == 0);
+            }
+          }
+        }
+      }
+    }
+    if (ok) {
+      const int slot = it % kAcRing;
+      if (it >= kAcRing) ok = warp_wait(&d_empty[slot], ((it / kAcRing) - 1) & 1);
+      if (ok && lane == 0) {
+        desc[slot].kind = 0;
+        mbar_arrive(&d_full[slot]);
+      }
+    }
+    // merge record: the item this CTA began and did not finish
+    if (lane == 0) {
+      int* rec = ws.rec + cta * 16;
+      rec[0] = rec_kind;
+      rec[1] = rec_last;
+      rec[2] = rw.row0;
+      rec[3] = rw.ntok;
+      rec[4] = rw.g;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ products
+    if (lane == 0) {
+      int pos = 0, nq = 0;
+      int np[2] = {0, 0};  // P tiles consumed
+      bool ok = true;
+      const uint64_t qd0 = sdesc_kmajor_sw128(smem_u32(sQ)), kd0 = sdesc_kmajor_sw128(smem_u32(sKV));
+      auto kv_wait = [&](int ps) { return mbar_wait(&kv_full[ps % NS], (ps / NS) & 1, a.status, sabort); };
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kAcRing;
+        if (!mbar_wait(&d_full[slot], (it / kAcRing) & 1, a.status, sabort)) break;
+        const int kind = desc[slot].kind, nc = desc[slot].nc;
+        if (kind == 0) break;
+        if (nc == 0) {
+          mbar_arrive(&d_empty[slot]);
+          continue;
+        }
+        const bool solo = kind == 2;
+        ok = mbar_wait(q_full, nq & 1, a.status, sabort);
+        if (!ok) break;
+        ++nq;
+        auto issue_s = [&](int w, int st) {
+          tc_fence_after();
+          const uint64_t qd = qd0 + ((solo ? 0 : w * C::kQ) >> 4), kd = kd0 + ((st * C::kStage) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            umma_bf16_ss(tmem + w * 128, qd + off, kd + off, C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[w]);
+        };
+        auto issue_pv = [&](int w, int st, bool first) -> bool {
+          if (!mbar_wait(&p_full[w], np[w] & 1, a.status, sabort)) return false;
+          ++np[w];
+          tc_fence_after();
+          const uint64_t vd = kd0 + ((st * C::kStage) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ts(tmem + kAcColO + w * D, tmem + w * 128 + kk * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4),
+                        C::kIdescO, (!first || kk > 0) ? 1u : 0u);
+          return true;
+        };
+        if (!solo) {
+          ok = kv_wait(pos);
+          if (!ok) break;
+          issue_s(0, pos % NS);
+          issue_s(1, pos % NS);
+          umma_commit(&kv_empty[pos % NS]);
+          ++pos;
+          for (int c = 0; c < nc && ok; ++c) {
+            const int vs = pos % NS, ks = (pos + 1) % NS;
+            const bool more = c + 1 < nc;
+            ok = kv_wait(pos) && issue_pv(0, vs, c == 0);
+            if (!ok) break;
+            if (more) {
+              ok = kv_wait(pos + 1);
+              if (!ok) break;
+              issue_s(0, ks);
+            } else {
+              umma_commit(&o_done[0]);
+            }
+            ok = issue_pv(1, vs, c == 0);
+            if (!ok) break;
+            umma_commit(&kv_empty[vs]);
+            if (more) {
+              issue_s(1, ks);
+              umma_commit(&kv_empty[ks]);
+            } else {
+              umma_commit(&o_done[1]);
+            }
+            pos += more ? 2 : 1;
+          }
+        } else {
+          for (int c = 0; c < min(2, nc) && ok; ++c) {
+            ok = kv_wait(pos);
+            if (!ok) break;
+            issue_s(c, pos % NS);
+            umma_commit(&kv_empty[pos % NS]);
+            ++pos;
+          }
+          for (int c = 0; c < nc && ok; ++c) {
+            const int w = c & 1;
+            ok = kv_wait(pos) && issue_pv(w, pos % NS, c < 2);
+            if (!ok) break;
+            umma_commit(&kv_empty[pos % NS]);
+            ++pos;
+            if (c + 2 < nc) {
+              ok = kv_wait(pos);
+              if (!ok) break;
+              issue_s(w, pos % NS);
+              umma_commit(&kv_empty[pos % NS]);
+              ++pos;
+            } else {
+              umma_commit(&o_done[w]);
+            }
+          }
+        }
+        if (ok) {
+          umma_commit(q_empty);
+          mbar_arrive(&d_empty[slot]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax and output
+    const int w = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tS = tl + w * 128, tO = tl + kAcColO + w * D;
+    const int rt = row / G, rh = row - rt * G;  // row within the tile, head within the group
+    const float sl2 = a.scale_log2, lazy = kAcLazy / sl2;
+    int ns = 0, no = 0, pos = 0;  // score tiles, items with chunks for this warpgroup, K/V ring position
+    int nx = 0;                   // meetings of the two warpgroups
+    bool ok = true;
+    auto meet = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_bar);
+      const bool met = warp_wait(x_bar, nx++ & 1);
+      tc_fence_after();
+      return met;
+    };
+    if (tid == 64) griddep_launch_dependents();
+    for (int it = 0; ok; ++it) {
+      const int dslot = it % kAcRing;
+      if (!warp_wait(&d_full[dslot], (it / kAcRing) & 1)) break;
+      const Work k = desc[dslot];
+      if (k.kind == 0) break;
+      const bool solo = k.kind == 2;
+      const int tok = (solo ? 0 : w * tpt) + rt;  // within the item
+      const bool valid = rt < tpt && tok < k.ntok;
+      const int t = k.t0 + tok;
+      // visible slots hid .. lim - 1 (rows past the item: never written, left unmasked)
+      const int lim = !valid ? 0x7fffffff : t >= k.nclean ? k.kv : k.base + t + 1;
+      const int lo_slot = valid ? k.hid : 0;
+      const int step = solo ? 2 : 1, first = solo ? w : 0;
+      const int lag = solo ? 2 : 1;
+      float m = -INFINITY, l = 0.f;
+      for (int c = first; c < k.nc; c += step) {
+        const int key0 = (k.c0 + c) * kAcKeys;
+        if (!warp_wait(&s_full[w], ns & 1)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32_nowait(tS + i * 32, s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait_ld32(s[i]);
+        if (__any_sync(0xffffffffu, key0 + kAcKeys > lim || key0 < lo_slot)) {
+          const int hi_c = lim - key0, lo_c = lo_slot - key0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (i * 32 + j >= hi_c || i * 32 + j < lo_c) s[i][j] = 0xFF800000u;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[i][j]));
+        // the reference maximum moves only past the headroom (or from -inf)
+        const bool move = mx > m + lazy || (m == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float m_new = move ? mx : m;
+          const float alpha = move ? ex2((m - m_new) * sl2) : 1.f;
+          l *= alpha;
+          m = m_new;
+          if (c >= step) {  // O of the earlier chunks: complete once this chunk's scores are
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 32) {
+              uint32_t o[32];
+              tmem_ld32_nowait(tO + cc, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32_nowait(tO + cc, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m * sl2;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int e = 2 * j;
+            const float p0 = ex2(fmaf(__uint_as_float(s[2 * i + (e >> 5)][e & 31]), sl2, neg));
+            const float p1 = ex2(fmaf(__uint_as_float(s[2 * i + (e >> 5)][(e & 31) + 1]), sl2, neg));
+            sum0 += p0;
+            sum1 += p1;
+            pk[j] = pack_bf16(p0, p1);
+          }
+          tmem_st32_nowait(tS + i * 32, pk);
+        }
+        l += sum0 + sum1;
+        // V of slots outside hidden .. kv - 1 may hold anything (stale pages, a
+        // page not loaded): 0 there, for 0 * NaN is not 0
+        if (key0 + kAcKeys > k.kv || key0 < k.hid) {
+          const int vp = pos + min(lag, k.nc) + c + min(c, max(0, k.nc - lag));
+          if (!warp_wait(&kv_full[vp % NS], (vp / NS) & 1)) {
+            ok = false;
+            break;
+          }
+          if (row < D) {
+            uint8_t* v = sKV + (vp % NS) * C::kStage + row * 128;
+#pragma unroll 1
+            for (int q = 0; q < 16; ++q) {
+              const int s0 = key0 + q * 8;
+              if (s0 + 8 <= k.kv && s0 >= k.hid) continue;
+              uint4* pv = reinterpret_cast<uint4*>(v + (q >> 3) * (D * 128) + (((q & 7) ^ (row & 7)) << 4));
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (s0 < k.kv && s0 + 8 > k.hid) {
+                x = *pv;
+                uint32_t* xe = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int sa = s0 + 2 * e;
+                  xe[e] &= ((sa < k.kv && sa >= k.hid) ? 0x0000FFFFu : 0u) |
+                           ((sa + 1 < k.kv && sa + 1 >= k.hid) ? 0xFFFF0000u : 0u);
+                }
+              }
+              *pv = x;
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      pos += 2 * k.nc;
+      if (!ok) break;
+      // ---------------------------------------------- the item's rows
+      const int mine_nc = (k.nc - first + step - 1) / step;  // chunks of this warpgroup
+      if (mine_nc > 0) {
+        if (!warp_wait(&o_done[w], no & 1)) break;
+        ++no;
+      }
+      tc_fence_after();
+      if (solo) {
+        // both warpgroups hold the same rows over alternate chunks: each
+        // finishes half of the features from both accumulators
+        sML[w * 128 + row] = make_float2(m, l);
+        if (!meet()) break;
+        const float2 o2 = sML[(w ^ 1) * 128 + row];
+        const float mm = fmaxf(m, o2.x);
+        const float a_own = m == -INFINITY ? 0.f : ex2((m - mm) * sl2);
+        const float a_oth = o2.x == -INFINITY ? 0.f : ex2((o2.x - mm) * sl2);
+        const float a0 = w == 0 ? a_own : a_oth, a1 = w == 0 ? a_oth : a_own;
+        const float lt = l * a_own + o2.y * a_oth;
+        const bool h0 = k.nc > 0, h1 = k.nc > 1;
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float f0 = k.slot < 0 ? a0 * inv : a0, f1 = k.slot < 0 ? a1 * inv : a1;
+        constexpr int HD = D / 2;
+#pragma unroll 1
+        for (int cc = 0; cc < HD; cc += 32) {
+          const int col = w * HD + cc;
+          uint32_t x[32], y[32];
+          tmem_ld32_nowait(tl + kAcColO + col, x);
+          tmem_ld32_nowait(tl + kAcColO + D + col, y);
+          tmem_wait_ld32(x);
+          tmem_wait_ld32(y);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            // an accumulator that no chunk reached holds anything
+            const float u = h0 && a0 > 0.f ? __uint_as_float(x[j]) * f0 : 0.f;
+            const float v = h1 && a1 > 0.f ? __uint_as_float(y[j]) * f1 : 0.f;
+            x[j] = __float_as_uint(u + v);
+          }
+          if (k.slot < 0) {
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(
+                  a.out + (static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh) * D + col);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint4 v4;
+                v4.x = pack_bf16(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]));
+                v4.y = pack_bf16(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]));
+                v4.z = pack_bf16(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]));
+                v4.w = pack_bf16(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7]));
+                dst[q] = v4;
+              }
+            }
+          } else if (valid) {
+            float* dst = ws.o + (static_cast<size_t>(cta * 2 + k.slot) * 2 * D + col) * 128 + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(x[j]);
+          }
+        }
+        if (w == 0 && valid) {
+          if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + row] = make_float2(mm, lt);
+          else if (a.lse)
+            a.lse[static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh] =
+                lt > 0.f ? (mm * sl2 + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+        }
+        if (!meet()) break;  // both accumulators and sML read
+      } else {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float f = k.slot < 0 ? inv : 1.f;
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t x[32];
+          tmem_ld32_nowait(tO + cc, x);
+          tmem_wait_ld32(x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = k.nc > 0 && l > 0.f ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
+          if (!valid) continue;
+          if (k.slot < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                a.out + (static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh) * D + cc);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4 v4;
+              v4.x = pack_bf16(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]));
+              v4.y = pack_bf16(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]));
+              v4.z = pack_bf16(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]));
+              v4.w = pack_bf16(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7]));
+              dst[q] = v4;
+            }
+          } else {
+            float* dst = ws.o + ((static_cast<size_t>(cta * 2 + k.slot) * 2 + w) * D + cc) * 128 + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(x[j]);
+          }
+        }
+        if (valid) {
+          if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + w * 128 + row] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh] =
+                l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_empty[dslot]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Rows of items that were cut: block (p, q) combines 32-row group q of the
+// item that CTA p began and others finished.  Partials are summed in CTA
+// order.  A warp takes D / 8 features, a lane a row.
+constexpr int kAmThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kAmThreads) attn_chunk_merge_kernel(const ChunkAttnArgs a, int P) {
+  griddep_wait();
+  const AcPart ws = ac_carve(a.workspace, P, D);
+  const int p0 = blockIdx.x;
+  const int* rec = ws.rec + p0 * 16;
+  const int kind = rec[0];
+  if (kind == 0) return;
+  const int tile = blockIdx.y >> 2, quarter = blockIdx.y & 3;
+  if (kind == 2 && tile > 0) return;
+  const int last = rec[1], row0 = rec[2], ntok = rec[3], g = rec[4];
+  const int G = a.Hq / a.Hkv, tpt = 128 / G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = quarter * 32 + lane;
+  const int rt = row / G, rh = row - rt * G, tok = tile * tpt + rt;
+  const bool valid = rt < tpt && tok < ntok;
+  if (!__any_sync(0xffffffffu, valid)) return;
+  constexpr int F = D / 8;
+  float acc[F];
+#pragma unroll
+  for (int j = 0; j < F; ++j) acc[j] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  auto slot_of = [&](int p) { return (p * 2 + (p == p0 ? 1 : 0)) * 2 + tile; };
+  if (valid) {
+    for (int p = p0; p <= last; ++p) m = fmaxf(m, ws.ml[slot_of(p) * 128 + row].x);
+    if (m > -INFINITY) {
+#pragma unroll 2
+      for (int p = p0; p <= last; ++p) {
+        const float2 ml = ws.ml[slot_of(p) * 128 + row];
+        if (ml.x == -INFINITY) continue;
+        const float e = ex2((ml.x - m) * a.scale_log2);
+        l += e * ml.y;
+        const float* o = ws.o + (static_cast<size_t>(slot_of(p)) * D + warp * F) * 128 + row;
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[j] += e * o[j * 128];
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
+    uint32_t pk[F / 2];
+#pragma unroll
+    for (int j = 0; j < F / 2; ++j) pk[j] = pack_bf16(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + warp * F);
+#pragma unroll
+    for (int q = 0; q < F / 8; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+    if (a.lse && warp == 0) a.lse[at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+namespace {
+template <int D>
+cudaError_t run_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkAttnArgs& a, int P,
+                      cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       AcCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  attn_chunk_kernel<D><<<P, kAcThreads, AcCfg<D>::kSmem, s>>>(q, k, v, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(P, 8);
+  cfg.blockDim = dim3(kAmThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_chunk_merge_kernel<D>, a, P);
+}
+}  // namespace
+
+cudaError_t launch_attn_chunk(const CUtensorMap& mapQ, const CUtensorMap& mapK, const CUtensorMap& mapV,
+                              const ChunkAttnArgs& a, int D, int P, cudaStream_t s) {
+  return D == 128 ? run_chunk<128>(mapQ, mapK, mapV, a, P, s) : run_chunk<64>(mapQ, mapK, mapV, a, P, s);
+}
+
+}  // namespace dvlm

@@ -373,6 +373,25 @@ struct MropeAppendArgs {
 };
 cudaError_t launch_mrope_append(const MropeAppendArgs& a, int D, cudaStream_t s);
 
+// Attention of ragged chunks of rows over paged caches (csrc/attn_chunk.cu).
+struct ChunkAttnArgs {
+  bf16* out;                  // [n_rows][Hq][D]
+  float* lse;                 // [n_rows][Hq] or NULL
+  const int32_t* block_table; // [n_batch][max_pages]
+  const int32_t* kv_len;      // [n_batch] slots, the new rows' included
+  const int32_t* cu_rows;     // [n_batch + 1]
+  const int32_t* n_noisy;     // [n_batch] or NULL (0): trailing rows that see every slot
+  const int32_t* n_hidden;    // [n_batch] or NULL (0): leading slots that no row sees
+  int n_batch, n_rows, n_pages, max_pages, Hq, Hkv;
+  float scale_log2;
+  void* workspace;
+  int* status;
+};
+size_t attn_chunk_scratch_bytes(int P, int D);
+// P: CTAs (one per SM).  q map: 3-D (D, Hq, rows), box (64, G, 128 / G).
+cudaError_t launch_attn_chunk(const CUtensorMap& mapQ, const CUtensorMap& mapK, const CUtensorMap& mapV,
+                              const ChunkAttnArgs& a, int D, int P, cudaStream_t s);
+
 // Failure-detection self-test of the bounded waits.
 cudaError_t launch_selftest_timeout(long long budget, int* status, int* waited_out, cudaStream_t s);
 // Block bookkeeping for the decode driver.

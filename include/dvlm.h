@@ -347,6 +347,43 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
                                             const int* sections, float rope_base, int interleaved,
                                             int* dev_status, dvlm_stream stream);
 
+/* Attention of ragged chunks of new rows -- single tokens, noisy blocks, prompt
+ * chunks, mixed in one call -- over paged caches.  q [n_rows, Hq, D] (row
+ * stride q_ld elements, a multiple of 8); request b owns rows cu_rows[b] ..
+ * cu_rows[b + 1] - 1, n_b of them; its cache holds kv_len[b] slots, the new
+ * rows' keys and values already in the last n_b.  Row t of n_b sits at slot
+ * s_t = kv_len[b] - n_b + t and sees slots n_hidden[b] .. s_t (C2C); the last
+ * n_noisy[b] rows see n_hidden[b] .. kv_len[b] - 1 (N2C and N2N) [Fast-dVLM
+ * technical overview (ocdem.com), section 2.2.1].  n_hidden (NULL: 0) hides a
+ * request's leading slots, as a TEXT-ONLY pass does [Look Only When Needed,
+ * method step (2)]; both are cut to 0 .. kv_len[b] and 0 .. n_b.  Query head h
+ * uses KV head h / (Hq / Hkv).  out [n_rows, Hq, D]: sum_j softmax_j(scale
+ * q.k_j) v_j over the visible slots j, 0 for a row that sees none; lse
+ * [n_rows, Hq] (fp32, may be NULL): the natural log of sum_j exp(scale
+ * q.k_j), -inf for such a row.  Rows before cu_rows[0] or behind
+ * cu_rows[n_batch] are left as they are.  Pages as in dvlm_block_attn_paged,
+ * with D == 64 or 128 and 1 <= Hq / Hkv <= 128; the page stores' rows
+ * (n_pages * Hkv * max(D, 64)) stay below 2^31.  scale > 0.  Hidden slots and
+ * those at or beyond kv_len[b] may hold anything, NaN included; the slots
+ * between must be finite.  Scores, softmax and sums in fp32, P in bf16.  The
+ * result of a row depends on the other requests of the call only in the
+ * order of its fp32 sums; the same call gives the same bits.  A request whose
+ * cu_rows descend or leave 0 .. n_rows, whose kv_len is outside 0 .. 64
+ * max_pages or below n_b, takes no part (DVLM_ERR_BOUNDS); a page number
+ * outside 0 .. n_pages - 1 sets DVLM_ERR_BOUNDS and page 0 is read.  cu_rows,
+ * kv_len, n_noisy, n_hidden, block_table [n_batch, max_pages]: device int32.
+ * workspace: dvlm_chunk_attn_paged_workspace_size bytes (device, 16-byte
+ * aligned, any contents; about 39 MB at D = 128); calls sharing one must not
+ * overlap.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED (other head shapes),
+ * WORKSPACE.  Two launches. */
+DVLM_API size_t dvlm_chunk_attn_paged_workspace_size(int n_batch, int n_rows, int Hq, int Hkv, int D);
+DVLM_API dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void* k_pages, const void* v_pages,
+                                          const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_rows,
+                                          const int32_t* n_noisy, const int32_t* n_hidden, float* lse, int n_batch,
+                                          int n_rows, int n_pages, int max_pages, int Hq, int Hkv, int D,
+                                          long long q_ld, float scale, void* workspace, size_t ws_bytes,
+                                          int* dev_status, dvlm_stream stream);
+
 /* Verification of drafted tokens against the target's probabilities from given
  * random numbers (the sampled counterpart of dvlm_spec_verify_accept: accepted
  * and drawn tokens together follow the target's distribution).  Per sequence

@@ -259,3 +259,29 @@ def test_step_binding_refuses_what_it_would_misread(dvlm_lib):
     for args in ((p.bfloat16(), None, i, u, u), (p[:, :4], None, i, u, u), (p, p[:, :3], i, u, u), (p, None, i, u.double(), u)):
         with pytest.raises(dv.DvlmError):
             dv.spec_verify_sample(*args, **vk)
+
+
+def _chunk(**kw):
+    a = dict(q=16, out=16, k=16, v=16, table=16, kv=16, cu=16, nb=2, rows=8, np=4, mp=4, Hq=8, Hkv=1, D=128, ld=1024,
+             scale=0.09, ws=16, wsb=1 << 40)
+    a.update(kw)
+    return dv.lib().dvlm_chunk_attn_paged(a["q"], a["out"], a["k"], a["v"], a["table"], a["kv"], a["cu"], None, None,
+                                          None, a["nb"], a["rows"], a["np"], a["mp"], a["Hq"], a["Hkv"], a["D"],
+                                          a["ld"], a["scale"], a["ws"], a["wsb"], None, None)
+
+
+def test_chunk_attention_host_validation(dvlm_lib):
+    for name in ("q", "out", "k", "v", "table", "kv", "cu"):
+        assert _chunk(**{name: None}) == INVALID
+    for name in ("q", "out", "k", "v", "ws"):
+        assert _chunk(**{name: 24}) == INVALID
+    for s in (0.0, -0.1, float("inf"), float("nan")):
+        assert _chunk(scale=s) == INVALID
+    for kw in (dict(nb=0), dict(rows=0), dict(np=0), dict(np=1 << 25), dict(mp=0), dict(Hq=0), dict(Hkv=3),
+               dict(ld=1016), dict(ld=1028), dict(np=1 << 24, Hkv=1), dict(np=1 << 20, Hkv=16, Hq=16, ld=2048)):
+        assert _chunk(**kw) == SHAPE, kw
+    assert _chunk(D=96) == UNSUPPORTED and _chunk(Hq=129, Hkv=1, ld=129 * 128) == UNSUPPORTED
+    assert _chunk(ws=None) == WORKSPACE and _chunk(wsb=1000) == WORKSPACE
+    assert dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 96) == 0
+    assert dv.chunk_attn_paged_workspace_size(0, 1, 16, 2, 128) == 0
+    assert 0 < dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 64) < dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 128)
