@@ -269,25 +269,39 @@ def selftest_wait_timeout(budget_cycles: int, status, gave_up, stream=None) -> N
 
 
 # ---------------------------------------------------------------- batched step over paged caches
-def _take(where: str, device, *args) -> None:
+def _take(where: str, dev: int, *args) -> None:
     """Refuse tensors the library would misread: args are (tensor, dtype, least
-    number of elements) triples; all contiguous, all on `device`."""
+    number of elements) triples; all contiguous, all on GPU number dev."""
     for t, dtype, least in args:
-        if t is not None and (t.dtype != dtype or t.numel() < least or t.device != device or not t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.numel() < least or t.get_device() != dev
+                              or not t.is_contiguous()):
             raise DvlmError(1, f"{where}: expected a contiguous {dtype} tensor of at least {least} elements on "
-                               f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                               f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _launch(fn, where: str, device, stream, *args) -> None:
-    """Call an entry point whose last argument is the stream with the tensors' device current."""
+def _device(where: str, t) -> int:
+    """GPU number of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise DvlmError(1, f"{where}: the tensors are on {t.device}, not on a GPU")
+    return dev
+
+
+def _launch(fn, where: str, dev: int, stream, *args) -> None:
+    """Call an entry point whose last argument is the stream, with GPU dev
+    current (a NULL stream is torch's current one on that GPU)."""
     import torch
-    if device.type != "cuda":
-        raise DvlmError(1, f"{where}: the tensors are on {device}, not on a GPU")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(fn(*args, stream_handle(stream)), where)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        _check(fn(*args, stream_handle(stream)), where)
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != 0:
+        raise DvlmError(status, where)
 
 
 _sections_cache: dict = {}
@@ -306,7 +320,7 @@ def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batc
               kv_len, cu_rows, slot_map, free_count_out, status=None, stream=None) -> None:
     """Block tables, row offsets and slot map of a ragged step (dvlm_page_plan)."""
     import torch
-    i32, dev = torch.int32, cache_len.device
+    i32, dev = torch.int32, _device("dvlm_page_plan", cache_len)
     _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
           (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
           (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
@@ -316,19 +330,22 @@ def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batc
             ptr(slot_map), ptr(free_count_out), ptr(status))
 
 
-def _rows(where: str, t, dtype, rows: int, ld: int, width: int, device) -> int:
-    """Row stride (elements) of a tensor whose rows of `width` elements lie ld apart (0: the
-    tensor's own first stride when it has one row per leading index and dense rows, else width)."""
-    if t.dtype != dtype or t.device != device:
-        raise DvlmError(1, f"{where}: expected a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-    if not ld:
-        inner = t[0] if t.dim() > 1 and t.shape[0] else t
-        if t.dim() > 1 and t.shape[0] >= rows and inner.numel() >= width and inner.is_contiguous():
-            return int(t.stride(0)) if t.shape[0] > 1 else max(int(inner.numel()), width)
-        ld = width
-    if not t.is_contiguous() or (rows > 0 and t.numel() < (rows - 1) * ld + width):
-        raise DvlmError(1, f"{where}: {tuple(t.shape)} does not hold {rows} rows of {width} elements {ld} apart")
-    return int(ld)
+def _rows(where: str, t, dtype, rows: int, ld: int, width: int, dev: int) -> int:
+    """Row stride (elements) of a tensor whose rows of `width` elements lie ld apart.  0: the tensor's
+    own first stride, its leading index counting the rows, or width for a dense tensor."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise DvlmError(1, f"{where}: expected a {dtype} tensor on cuda:{dev}, got {t.dtype} on {t.device}")
+    if rows < 1:
+        return ld or width  # (the library refuses the call)
+    if t.is_contiguous():
+        if not ld:
+            ld = t.numel() // t.shape[0] if t.dim() > 1 and t.shape[0] >= rows and t.numel() >= rows * width else width
+        if t.numel() >= (rows - 1) * ld + width:
+            return ld
+    elif not ld and t.dim() > 1 and t.shape[0] >= rows and t[0].numel() >= width and t[0].is_contiguous():
+        return t.stride(0)
+    raise DvlmError(1, f"{where}: {tuple(t.shape)} does not hold {rows} rows of {width} elements "
+                       f"{ld or 'any distance'} apart")
 
 
 def mrope(x, out, pos, *, n_rows, n_heads, D, sections, rope_base, dtype, rot_dim=0, interleaved=0, x_ld=0, out_ld=0,
@@ -336,7 +353,7 @@ def mrope(x, out, pos, *, n_rows, n_heads, D, sections, rope_base, dtype, rot_di
     """Rotary positions with len(sections) axes on rows of heads (dvlm_mrope).  rot_dim 0: D.
     Row strides 0: taken from the tensors (rows may be slices of wider rows)."""
     import torch
-    dev, td = x.device, torch.float32 if dtype == DVLM_FP32 else torch.bfloat16
+    dev, td = _device("dvlm_mrope", x), torch.float32 if dtype == DVLM_FP32 else torch.bfloat16
     x_ld = _rows("dvlm_mrope", x, td, n_rows, x_ld, n_heads * D, dev)
     out_ld = _rows("dvlm_mrope", out, td, n_rows, out_ld, n_heads * D, dev)
     sec = _sections(sections)
@@ -349,7 +366,7 @@ def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, H
                        rope_base, rot_dim=0, interleaved=0, qkv_ld=0, status=None, stream=None) -> None:
     """Rotate queries and keys and write keys and values into their pages (dvlm_mrope_append_paged)."""
     import torch
-    dev, bf = qkv.device, torch.bfloat16
+    dev, bf = _device("dvlm_mrope_append_paged", qkv), torch.bfloat16
     qkv_ld = _rows("dvlm_mrope_append_paged", qkv, bf, n_rows, qkv_ld, (Hq + 2 * Hkv) * D, dev)
     sec = _sections(sections)
     _take("dvlm_mrope_append_paged", dev, (pos, torch.int32, len(sec) * n_rows), (slot_map, torch.int32, n_rows),
@@ -369,12 +386,14 @@ def chunk_attn_paged(q, out, k_pages, v_pages, block_table, kv_len, cu_rows, *, 
                      stream=None) -> None:
     """Attention of ragged chunks of rows over paged caches (dvlm_chunk_attn_paged)."""
     import torch
-    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
+    dev, bf, i32 = _device("dvlm_chunk_attn_paged", q), torch.bfloat16, torch.int32
     q_ld = _rows("dvlm_chunk_attn_paged", q, bf, n_rows, q_ld, Hq * D, dev)
     _take("dvlm_chunk_attn_paged", dev, (out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
           (v_pages, bf, n_pages * Hkv * 64 * D), (block_table, i32, n_batch * max_pages), (kv_len, i32, n_batch),
           (cu_rows, i32, n_batch + 1), (n_noisy, i32, n_batch), (n_hidden, i32, n_batch),
           (lse, torch.float32, n_rows * Hq), (status, i32, 1))
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise DvlmError(1, f"dvlm_chunk_attn_paged: the workspace is not a contiguous tensor on cuda:{dev}")
     _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, ptr(q), ptr(out), ptr(k_pages),
             ptr(v_pages), ptr(block_table), ptr(kv_len), ptr(cu_rows), ptr(n_noisy), ptr(n_hidden), ptr(lse), n_batch,
             n_rows, n_pages, max_pages, Hq, Hkv, D, q_ld, float(scale), ptr(workspace),
@@ -385,7 +404,7 @@ def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K
                        n_draft=None, cache_len=None, cache_len_out=None, status=None, stream=None) -> None:
     """Verify drafts by rejection sampling with given random numbers (dvlm_spec_verify_sample)."""
     import torch
-    dev, i32, f32 = target_p.device, torch.int32, torch.float32
+    dev, i32, f32 = _device("dvlm_spec_verify_sample", target_p), torch.int32, torch.float32
     td = f32 if dtype == DVLM_FP32 else torch.bfloat16
     _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
           (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),

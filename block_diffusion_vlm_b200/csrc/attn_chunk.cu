@@ -37,21 +37,22 @@ namespace dvlm {
 
 namespace {
 constexpr int kAcThreads = 320;  // warp 0 loads and schedules, 1 issues MMAs, 2..5 and 6..9 softmax
-constexpr int kAcKeys = 128;     // slots per chunk: two pages
+constexpr int kAcKeys = 64;      // slots per step: one page
 constexpr int kAcRing = 4;       // work descriptors in flight
 constexpr int kAcItemCost = 256; // fixed cost of an item, in slot units (prologue and epilogue)
-constexpr int kAcMinPart = 384;  // least cost worth a CTA of its own
+constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
+constexpr int kAcPrefetch = 8;   // pages brought into L2 ahead of the ring (solo items)
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
 template <int D>
 struct AcCfg {
-  static constexpr int kStage = kAcKeys * D * 2;  // one K or V^T chunk
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStage = kAcKeys * D * 2;  // one K or V^T page
+  static constexpr int kStages = D == 128 ? 8 : 12;
   static constexpr int kQ = 128 * D * 2;          // one Q tile
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kQ;
   static constexpr int oBar = oKV + kStages * kStage;
-  static constexpr int kBars = 2 * kAcRing + 2 + 2 * kStages + 7;
+  static constexpr int kBars = 2 * kAcRing + 2 + 2 * kStages + 4 + 4 + 2 + 2 + 1;
   static constexpr int oDesc = oBar + 512;
   static constexpr int oML = oDesc + kAcRing * 64;
   static constexpr int kSmem = oML + 2 * 128 * 8 + 1024;
@@ -148,12 +149,151 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t 
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// The rest of a wait that did not end at once, by a whole warp (out of line:
+// the loops stay short).
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort_flag)) != 0;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) { return ex2_approx(x); }
+
+// Two fp32 lanes in one 64-bit register (packed multiply-add and add).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x for two x >= -126 on the multiply-add pipe: x = n + r with n the nearest
+// integer (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^r by the
+// cubic of least relative error on [-1/2, 1/2] (7.5e-5, a Lawson-weighted
+// least-squares fit; P is rounded to bf16, 3.9e-3, right after), n added to the
+// exponent field.
+__device__ __forceinline__ void ex2_poly2(uint64_t x, float& y0, float& y1) {
+  constexpr float kMagic = 12582912.f;
+  const uint64_t t = add2(x, pack2(kMagic, kMagic));
+  const uint64_t n = add2(t, pack2(-kMagic, -kMagic));
+  const uint64_t r = fma2(n, pack2(-1.f, -1.f), x);
+  uint64_t p = fma2(r, pack2(0.05517167f, 0.05517167f), pack2(0.24261113f, 0.24261113f));
+  p = fma2(p, r, pack2(0.69326097f, 0.69326097f));
+  p = fma2(p, r, pack2(0.99992806f, 0.99992806f));
+  float t0, t1, p0, p1;
+  unpack2(t, t0, t1);
+  unpack2(p, p0, p1);
+  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+// p_j = 2^(sl2 s_j + neg) of a 32-column block of scores, packed to bf16;
+// returns their fp32 sum.  kPoly of every 4 pairs go to the polynomial: the
+// exponential unit gives 16 results a clock and SM, which alone would take as
+// long as the products of the tile.  A masked score (-inf) gives 0, or 2^-126
+// from the polynomial: nothing beside any visible slot of the row, and a row
+// without one keeps its maximum at -inf and is set to 0 at the end.
+template <int kPoly>
+__device__ __forceinline__ float exp_block(const uint32_t (&s)[32], uint64_t sl2, uint64_t neg, uint32_t* pk) {
+  uint64_t sum = pack2(0.f, 0.f), sum1 = sum;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sl2, neg);
+    float x0, x1, p0, p1;
+    unpack2(x, x0, x1);
+    if ((j & 3) < kPoly) {
+      ex2_poly2(pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f)), p0, p1);
+    } else {
+      p0 = ex2(x0);
+      p1 = ex2(x1);
+    }
+    if (j & 1) sum1 = add2(sum1, pack2(p0, p1));
+    else sum = add2(sum, pack2(p0, p1));
+    pk[j] = pack_bf16(p0, p1);
+  }
+  float u, v;
+  unpack2(add2(sum, sum1), u, v);
+  return u + v;
+}
+constexpr int kAcPoly = 0;
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Largest of m and 32 values, in two chains.
+__device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
+  float m1 = __uint_as_float(s[0]);
+#pragma unroll
+  for (int j = 1; j < 29; j += 4) {
+    m = max3(m, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+    m1 = max3(m1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+  }
+  return max3(max3(m, __uint_as_float(s[29]), __uint_as_float(s[30])), m1, __uint_as_float(s[31]));
+}
+
+// Scores of a 32-slot block outside slots lo .. hi - 1 to -inf.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int hi, int lo) {
+  const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t keep = below & (lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : ~((1u << lo) - 1u));
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (!(keep >> j & 1u)) s[j] = 0xFF800000u;
+}
+// One feature's row of a V^T page (64 slots, 128-byte swizzle): 0 outside
+// slots lo .. hi - 1.
+__device__ __noinline__ void clear_outside(uint8_t* v, int sw, int hi, int lo) {
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    const int s = q * 8;
+    if (s + 8 <= hi && s >= lo) continue;
+    uint4* pv = reinterpret_cast<uint4*>(v + ((q ^ sw) << 4));
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (s < hi && s + 8 > lo) {
+      x = *pv;
+      uint32_t* xe = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int sa = s + 2 * e;
+        xe[e] &= ((sa < hi && sa >= lo) ? 0x0000FFFFu : 0u) | ((sa + 1 < hi && sa + 1 >= lo) ? 0xFFFF0000u : 0u);
+      }
+    }
+    *pv = x;
+  }
+}
+
+// floor(a / b) for a >= 0, b > 0 with a quotient below 2^20: a float estimate
+// put right (64-bit integer division costs hundreds of cycles on the one warp
+// that everything waits for).
+__device__ __forceinline__ int div_small(long long a, long long b) {
+  int q = static_cast<int>(static_cast<float>(a) / static_cast<float>(b));
+  while (q > 0 && q * b > a) --q;
+  while ((q + 1) * b <= a) ++q;
+  return q;
+}
 }  // namespace
 
 // Partial results in the workspace: per CTA two slots of two tiles, O [D][128]
@@ -195,9 +335,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   uint64_t* q_empty = q_full + 1;          // every S of the item done
   uint64_t* kv_full = q_empty + 1;         // [NS]
   uint64_t* kv_empty = kv_full + NS;       // [NS]
-  uint64_t* s_full = kv_empty + NS;        // [2] scores of a chunk (and all earlier products) done
-  uint64_t* p_full = s_full + 2;           // [2] P written, O rescaled
-  uint64_t* o_done = p_full + 2;           // [2] last P V of the item done
+  uint64_t* s_full = kv_empty + NS;        // [2 tiles][2 buffers] scores of a page done
+  uint64_t* p_full = s_full + 4;           // [2][2] P written, O rescaled
+  uint64_t* pv_done = p_full + 4;          // [2] P V of a page done (one phase per page)
+  uint64_t* o_done = pv_done + 2;          // [2] last P V of the item done (pv_done may be two phases behind there)
   uint64_t* x_bar = o_done + 2;            // the softmax warps of both tiles meet (a bounded wait, unlike bar.sync)
   static_assert(C::kBars * 8 + 16 <= 512, "barrier space");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
@@ -205,7 +346,9 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   Work* desc = reinterpret_cast<Work*>(smem + C::oDesc);
   float2* sML = reinterpret_cast<float2*>(smem + C::oML);  // [2][128] solo: both warpgroups' (m, l)
   __shared__ long long s_scan[kAcThreads / 32];
-  __shared__ long long s_find[2];  // (request, its first cost) holding this CTA's first unit
+  __shared__ long long s_start;  // cost position, number and lengths of the request with this CTA's first unit
+  __shared__ int s_b;
+  __shared__ Req s_req;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = gridDim.x, cta = blockIdx.x;
@@ -215,7 +358,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < C::kBars; ++i) {
       uint64_t* b = &bars[i];
-      mbar_init(b, (b >= d_empty && b < q_full) ? 9 : (b >= p_full && b < o_done) ? 4 : b == x_bar ? 8 : 1);
+      mbar_init(b, (b >= d_empty && b < q_full) ? 9 : (b >= p_full && b < pv_done) ? 4 : b == x_bar ? 8 : 1);
     }
     *sabort = 0;
     fence_mbar_init();
@@ -229,11 +372,22 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   }
 
   // ------------------------------------------------ this CTA's part of the line
+  // (a float estimate of the share: every CTA computes the same one, and the
+  // shares need only cover the line)
   const int per = (a.n_batch + kAcThreads - 1) / kAcThreads;
   const int b0 = min(a.n_batch, tid * per), b1 = min(a.n_batch, b0 + per);
   int bad = 0;
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += a.Hkv * req_cost(load_req(a, b, tpt, &bad), tpt);
+  long long mine = 0, c0 = 0;
+  Req r0{};
+  for (int b = b0; b < b1; ++b) {
+    const Req r = load_req(a, b, tpt, &bad);
+    const long long c = a.Hkv * req_cost(r, tpt);
+    if (b == b0) {
+      r0 = r;
+      c0 = c;
+    }
+    mine += c;
+  }
   if (bad && cta == 0) record_error(a.status, DVLM_ERR_BOUNDS);
   long long inc = mine;
 #pragma unroll
@@ -251,27 +405,28 @@ __global__ void __launch_bounds__(kAcThreads, 1)
     if (w == warp) before = total;
     total += s_scan[w];
   }
-  const long long parts = max(1LL, min(static_cast<long long>(P), total / kAcMinPart));
-  const long long lo = cta < parts ? total * cta / parts : total;
-  const long long hi = cta < parts ? total * (cta + 1) / parts : total;
+  const int parts = max(1, min(P, static_cast<int>(min(1.0e6f, static_cast<float>(total) * (1.f / kAcMinPart)))));
+  const long long share = static_cast<long long>(static_cast<float>(total) * 1.000001f / parts) + 1;
+  const long long lo = min(total, cta * share), hi = min(total, lo + share);
   long long at = before + inc - mine;
   if (lo < hi && at <= lo && lo < at + mine) {  // one thread's requests hold the first unit
-    for (int b = b0; b < b1; ++b) {
-      const long long c = a.Hkv * req_cost(load_req(a, b, tpt, &bad), tpt);
-      if (lo < at + c) {
-        s_find[0] = b;
-        s_find[1] = at;
-        break;
-      }
-      at += c;
+    int b = b0;
+    while (lo >= at + c0) {
+      at += c0;
+      r0 = load_req(a, ++b, tpt, &bad);
+      c0 = a.Hkv * req_cost(r0, tpt);
     }
+    s_b = b;
+    s_start = at;
+    s_req = r0;
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
 
   // whole warps wait as one: either every lane goes on or none does
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, sabort)) != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_longer(bar, parity, a.status, sabort);
   };
 
   if (warp == 0) {
@@ -285,23 +440,22 @@ __global__ void __launch_bounds__(kAcThreads, 1)
     Work rw{};
     int rec_last = 0;
     if (lo < hi) {
-      int b = static_cast<int>(s_find[0]);
-      long long start = s_find[1];  // cost position of the current item
-      Req r = load_req(a, b, tpt, &bad);
-      long long per_head = req_cost(r, tpt);
-      int g = static_cast<int>((lo - start) / per_head);
+      int b = s_b;
+      long long start = s_start;  // cost position of the current item
+      Req r = s_req;
+      const long long per_head = req_cost(r, tpt);
+      int g = div_small(lo - start, per_head);
       start += g * per_head;
+      // last item whose prefix is at or below lo, 32 candidates at a time
       int i = 0;
-      {  // last item whose prefix is at or below lo
-        int l = 0, h = r.pairs + r.solo;
-        while (h - l > 1) {
-          const int m = (l + h) >> 1;
-          if (start + pair_prefix(r, tpt, m) <= lo) l = m;
-          else h = m;
-        }
-        i = l;
-        start += pair_prefix(r, tpt, i);
+      const int n_items = r.pairs + r.solo;
+      for (int span = n_items; span > 1;) {
+        const int step = (span + 31) >> 5, cand = i + lane * step;
+        const bool below = lane * step < span && cand < n_items && start + pair_prefix(r, tpt, cand) <= lo;
+        i += (31 - __clz(__ballot_sync(0xffffffffu, below))) * step;
+        span = step;
       }
+      start += pair_prefix(r, tpt, i);
       long long x = lo;
       while (x < hi && ok) {
         const bool solo = i == r.pairs;
@@ -323,16 +477,18 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const int cb = r.hid / kAcKeys, nch = end > r.hid ? (end + kAcKeys - 1) / kAcKeys - cb : 0;
         // cut positions in chunks; a solo item is cut in pairs of chunks
         const int unit = solo ? 2 : 1;
-        const long long nu = (nch + unit - 1) / unit;
-        const int ca = static_cast<int>(nu * xa / w) * unit;
-        const int ce = xb == w ? nch : static_cast<int>(nu * xb / w) * unit;
+        // (the CTA that ends here and the one that goes on compute the same cut)
+        const int nu = (nch + unit - 1) / unit;
+        const float scale = static_cast<float>(nu) / static_cast<float>(w);
+        const int ca = min(nu, static_cast<int>(static_cast<float>(xa) * scale)) * unit;
+        const int ce = xb == w ? nch : min(nu, static_cast<int>(static_cast<float>(xb) * scale)) * unit;
         k.c0 = cb + ca;
-        k.nc = max(0, min(ce, nch) - ca);
+        k.nc = max(0, min(ce, nch) - min(ca, nch));
         k.slot = (xa == 0 && xb == w) ? -1 : (xa == 0 ? 1 : 0);
         if (k.slot == 1) {  // the item goes on: the CTA that holds its last unit
           rec_kind = k.kind;
           rw = k;
-          rec_last = static_cast<int>(((start + w) * parts - 1) / total);
+          rec_last = div_small(start + w - 1, share);
         }
         // hand the descriptor over
         const int slot = it % kAcRing;
@@ -355,50 +511,63 @@ __global__ void __launch_bounds__(kAcThreads, 1)
                 tma_load_3d(sQ + w2 * C::kQ + d * 16384, &mapQ, q_full, d * 64, g * G, k.row0 + w2 * tpt, pol);
           }
           ++nq;
-          // K and V in the order the products take them: K of the first chunk
-          // (two for a solo item), then V(c), K(c + lag)
-          const int lag = k.kind == 1 ? 1 : 2;
+          // K and V in the order the products take them: K of the first pages
+          // (two of each tile's buffers), then V(c), K(c + lag)
+          const int lag = k.kind == 1 ? 2 : 4;
           const int n_held = (r.kv + 63) >> 6;
-          int page_base = -1, page_v = 0;
-          auto page_of = [&](int p) -> int {  // logical page -> page number, 32 at a time
-            if (page_base < 0 || p < page_base || p >= page_base + 32) {
-              page_base = p;
-              page_v = 0;
-              if (p + lane < n_held) {
-                page_v = a.block_table[static_cast<size_t>(b) * a.max_pages + p + lane];
-                if (page_v < 0 || page_v >= a.n_pages) {
-                  record_error(a.status, DVLM_ERR_BOUNDS);
-                  page_v = 0;
-                }
-              }
-            }
-            return __shfl_sync(0xffffffffu, page_v, p - page_base);
+          // page numbers: a window of 64 table entries, two per lane, that
+          // moves up by 32 (loads, prefetches and the lagging V stay within 32)
+          const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
+          int win = k.c0 & ~31;
+          auto entry_at = [&](int p) -> int {
+            if (p >= n_held) return 0;
+            const int v = table[p];
+            if (v >= 0 && v < a.n_pages) return v;
+            record_error(a.status, DVLM_ERR_BOUNDS);
+            return 0;
           };
-          // K runs ahead of V: one lookup window each would thrash, so a
-          // window starts at V's page and spans K's
+          int w0 = entry_at(win + lane), w1 = entry_at(win + 32 + lane);
+          auto page_of = [&](int p) -> int {
+            if (p >= win + 64) {
+              win += 32;
+              w0 = w1;
+              w1 = entry_at(win + 32 + lane);
+            }
+            return __shfl_sync(0xffffffffu, p < win + 32 ? w0 : w1, p & 31);
+          };
           auto load = [&](int c, bool is_v) {
             const int st = pos % NS;
             if (pos >= NS) ok = warp_wait(&kv_empty[st], ((pos / NS) - 1) & 1);
             if (!ok) return;
-            const int p0 = 2 * (k.c0 + c), np = p0 + 1 < n_held ? 2 : 1;
-            const int pg0 = page_of(p0), pg1 = np == 2 ? page_of(p0 + 1) : 0;
+            const int entry = page_of(k.c0 + c) * a.Hkv + g;
             if (lane == 0) {
-              mbar_arrive_expect_tx(&kv_full[st], np * 64 * D * 2);
+              mbar_arrive_expect_tx(&kv_full[st], C::kStage);
               uint8_t* dst = sKV + st * C::kStage;
-              for (int h = 0; h < np; ++h) {
-                const int entry = (h ? pg1 : pg0) * a.Hkv + g;
-                if (is_v) {
-                  tma_load_2d(dst + h * (D * 128), &mapV, &kv_full[st], 0, entry * D, pol);
-                } else {
-                  for (int d = 0; d < D / 64; ++d)
-                    tma_load_2d(dst + d * 16384 + h * 8192, &mapK, &kv_full[st], d * 64, entry * 64, pol);
-                }
+              if (is_v) {
+                tma_load_2d(dst, &mapV, &kv_full[st], 0, entry * D, pol);
+              } else {
+                for (int d = 0; d < D / 64; ++d)
+                  tma_load_2d(dst + d * 8192, &mapK, &kv_full[st], d * 64, entry * 64, pol);
               }
             }
             ++pos;
           };
+          // The ring holds two chunks.  Where few rows read a long cache (solo)
+          // the chunks behind them are brought into L2 ahead, so that a freed
+          // stage refills at L2's latency: 64 single tokens over 900 to 16000
+          // slots
+          auto prefetch = [&](int c) {
+            const int entry = page_of(k.c0 + c) * a.Hkv + g;
+            if (lane == 0) {
+              for (int d = 0; d < D / 64; ++d) tma_prefetch_2d(&mapK, d * 64, entry * 64);
+              tma_prefetch_2d(&mapV, 0, entry * D);
+            }
+          };
+          int pf = lag;
           for (int c = 0; c < min(lag, k.nc) && ok; ++c) load(c, false);
           for (int c = 0; c < k.nc && ok; ++c) {
+            if (k.kind == 2)
+              for (; pf < k.nc && pf <= c + lag + kAcPrefetch; ++pf) prefetch(pf);
             load(c, true);
             if (ok && c + lag < k.nc) load(c + lag, false);
           }
@@ -439,9 +608,11 @@ __global__ void __launch_bounds__(kAcThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
+    // (elect.sync rather than lane == 0: the compiler then keeps descriptors
+    // in uniform registers and issues a product in half the instructions)
+    if (elect_one()) {
       int pos = 0, nq = 0;
-      int np[2] = {0, 0};  // P tiles consumed
+      int ni[2] = {0, 0}, np[2] = {0, 0};  // per tile: scores issued, P pages consumed (buffer = parity)
       bool ok = true;
       const uint64_t qd0 = sdesc_kmajor_sw128(smem_u32(sQ)), kd0 = sdesc_kmajor_sw128(smem_u32(sKV));
       auto kv_wait = [&](int ps) { return mbar_wait(&kv_full[ps % NS], (ps / NS) & 1, a.status, sabort); };
@@ -460,79 +631,62 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         ++nq;
         auto issue_s = [&](int w, int st) {
           tc_fence_after();
+          const int buf = ni[w]++ & 1;
           const uint64_t qd = qd0 + ((solo ? 0 : w * C::kQ) >> 4), kd = kd0 + ((st * C::kStage) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            umma_bf16_ss(tmem + w * 128, qd + off, kd + off, C::kIdescS, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&s_full[w]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ss(tmem + w * 128 + buf * 64, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                         kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+          umma_commit(&s_full[w * 2 + buf]);
         };
-        auto issue_pv = [&](int w, int st, bool first) -> bool {
-          if (!mbar_wait(&p_full[w], np[w] & 1, a.status, sabort)) return false;
+        auto issue_pv = [&](int w, int st, bool first, bool last) -> bool {
+          const int buf = np[w] & 1;
+          if (!mbar_wait(&p_full[w * 2 + buf], (np[w] >> 1) & 1, a.status, sabort)) return false;
           ++np[w];
           tc_fence_after();
           const uint64_t vd = kd0 + ((st * C::kStage) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_f16_ts(tmem + kAcColO + w * D, tmem + w * 128 + kk * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4),
-                        C::kIdescO, (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ts(tmem + kAcColO + w * D, tmem + w * 128 + buf * 64 + kk * 8, vd + ((kk * 32) >> 4), C::kIdescO,
+                        (!first || kk > 0) ? 1u : 0u);
+          umma_commit(&pv_done[w]);
+          if (last) umma_commit(&o_done[w]);
           return true;
         };
-        if (!solo) {
+        const int lag = solo ? 4 : 2;
+        for (int c = 0; c < min(lag, nc) && ok; ++c) {
           ok = kv_wait(pos);
           if (!ok) break;
-          issue_s(0, pos % NS);
-          issue_s(1, pos % NS);
+          if (solo) {
+            issue_s(c & 1, pos % NS);
+          } else {
+            issue_s(0, pos % NS);
+            issue_s(1, pos % NS);
+          }
           umma_commit(&kv_empty[pos % NS]);
           ++pos;
-          for (int c = 0; c < nc && ok; ++c) {
-            const int vs = pos % NS, ks = (pos + 1) % NS;
-            const bool more = c + 1 < nc;
-            ok = kv_wait(pos) && issue_pv(0, vs, c == 0);
-            if (!ok) break;
-            if (more) {
-              ok = kv_wait(pos + 1);
-              if (!ok) break;
-              issue_s(0, ks);
-            } else {
-              umma_commit(&o_done[0]);
-            }
-            ok = issue_pv(1, vs, c == 0);
+        }
+        for (int c = 0; c < nc && ok; ++c) {
+          const int vs = pos % NS, ks = (pos + 1) % NS;
+          const bool more = c + lag < nc;
+          ok = kv_wait(pos) && (!more || kv_wait(pos + 1));
+          if (!ok) break;
+          if (solo) {
+            ok = issue_pv(c & 1, vs, c < 2, c + 2 >= nc);
             if (!ok) break;
             umma_commit(&kv_empty[vs]);
-            if (more) {
-              issue_s(1, ks);
-              umma_commit(&kv_empty[ks]);
-            } else {
-              umma_commit(&o_done[1]);
-            }
-            pos += more ? 2 : 1;
-          }
-        } else {
-          for (int c = 0; c < min(2, nc) && ok; ++c) {
-            ok = kv_wait(pos);
+            if (more) issue_s(c & 1, ks);
+          } else {
+            ok = issue_pv(0, vs, c == 0, c + 1 == nc);
             if (!ok) break;
-            issue_s(c, pos % NS);
-            umma_commit(&kv_empty[pos % NS]);
-            ++pos;
-          }
-          for (int c = 0; c < nc && ok; ++c) {
-            const int w = c & 1;
-            ok = kv_wait(pos) && issue_pv(w, pos % NS, c < 2);
+            if (more) issue_s(0, ks);
+            ok = issue_pv(1, vs, c == 0, c + 1 == nc);
             if (!ok) break;
-            umma_commit(&kv_empty[pos % NS]);
-            ++pos;
-            if (c + 2 < nc) {
-              ok = kv_wait(pos);
-              if (!ok) break;
-              issue_s(w, pos % NS);
-              umma_commit(&kv_empty[pos % NS]);
-              ++pos;
-            } else {
-              umma_commit(&o_done[w]);
-            }
+            umma_commit(&kv_empty[vs]);
+            if (more) issue_s(1, ks);
           }
+          if (more) umma_commit(&kv_empty[ks]);
+          pos += more ? 2 : 1;
         }
         if (ok) {
           umma_commit(q_empty);
@@ -547,8 +701,9 @@ __global__ void __launch_bounds__(kAcThreads, 1)
     const uint32_t tS = tl + w * 128, tO = tl + kAcColO + w * D;
     const int rt = row / G, rh = row - rt * G;  // row within the tile, head within the group
     const float sl2 = a.scale_log2, lazy = kAcLazy / sl2;
-    int ns = 0, no = 0, pos = 0;  // score tiles, items with chunks for this warpgroup, K/V ring position
-    int nx = 0;                   // meetings of the two warpgroups
+    int ns = 0, pos = 0;  // pages of this tile, K/V ring position
+    int no = 0;           // items with pages for this tile
+    int nx = 0;           // meetings of the two warpgroups
     bool ok = true;
     auto meet = [&]() {
       tc_fence_before();
@@ -557,6 +712,20 @@ __global__ void __launch_bounds__(kAcThreads, 1)
       const bool met = warp_wait(x_bar, nx++ & 1);
       tc_fence_after();
       return met;
+    };
+    // 16 features of this thread's row: to the output, or to this CTA's partial slot
+    auto store_cols = [&](const Work& k, int tok, bool valid, int tile, int col, const float (&x)[16]) {
+      if (!valid) return;
+      if (k.slot < 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh) * D + col);
+        dst[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        dst[1] = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]),
+                            pack_bf16(x[14], x[15]));
+      } else {
+        float* dst = ws.o + ((static_cast<size_t>(cta * 2 + k.slot) * 2 + tile) * D + col) * 128 + row;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dst[j * 128] = x[j];
+      }
     };
     if (tid == 64) griddep_launch_dependents();
     for (int it = 0; ok; ++it) {
@@ -567,119 +736,85 @@ __global__ void __launch_bounds__(kAcThreads, 1)
       const bool solo = k.kind == 2;
       const int tok = (solo ? 0 : w * tpt) + rt;  // within the item
       const bool valid = rt < tpt && tok < k.ntok;
+      const bool live = __any_sync(0xffffffffu, valid);
       const int t = k.t0 + tok;
       // visible slots hid .. lim - 1 (rows past the item: never written, left unmasked)
       const int lim = !valid ? 0x7fffffff : t >= k.nclean ? k.kv : k.base + t + 1;
       const int lo_slot = valid ? k.hid : 0;
       const int step = solo ? 2 : 1, first = solo ? w : 0;
-      const int lag = solo ? 2 : 1;
+      const int lag = solo ? 4 : 2;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int c = first; c < k.nc; c += step) {
-        const int key0 = (k.c0 + c) * kAcKeys;
-        if (!warp_wait(&s_full[w], ns & 1)) {
+        const int key0 = (k.c0 + c) * kAcKeys, buf = ns & 1;
+        if (!warp_wait(&s_full[w * 2 + buf], (ns >> 1) & 1)) {
           ok = false;
           break;
         }
         ++ns;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_nowait(tS + i * 32, s[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait_ld32(s[i]);
-        if (__any_sync(0xffffffffu, key0 + kAcKeys > lim || key0 < lo_slot)) {
-          const int hi_c = lim - key0, lo_c = lo_slot - key0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (i * 32 + j >= hi_c || i * 32 + j < lo_c) s[i][j] = 0xFF800000u;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[i][j]));
-        // the reference maximum moves only past the headroom (or from -inf)
-        const bool move = mx > m + lazy || (m == -INFINITY && mx > -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? mx : m;
-          const float alpha = move ? ex2((m - m_new) * sl2) : 1.f;
-          l *= alpha;
-          m = m_new;
-          if (c >= step) {  // O of the earlier chunks: complete once this chunk's scores are
-#pragma unroll 1
-            for (int cc = 0; cc < D; cc += 32) {
-              uint32_t o[32];
-              tmem_ld32_nowait(tO + cc, o);
-              tmem_wait_ld32(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32_nowait(tO + cc, o);
-            }
-          }
-        }
-        const float neg = m == -INFINITY ? 0.f : -m * sl2;
-        float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int e = 2 * j;
-            const float p0 = ex2(fmaf(__uint_as_float(s[2 * i + (e >> 5)][e & 31]), sl2, neg));
-            const float p1 = ex2(fmaf(__uint_as_float(s[2 * i + (e >> 5)][(e & 31) + 1]), sl2, neg));
-            sum0 += p0;
-            sum1 += p1;
-            pk[j] = pack_bf16(p0, p1);
-          }
-          tmem_st32_nowait(tS + i * 32, pk);
-        }
-        l += sum0 + sum1;
-        // V of slots outside hidden .. kv - 1 may hold anything (stale pages, a
-        // page not loaded): 0 there, for 0 * NaN is not 0
+        const uint32_t tP = tS + buf * 64;
+        uint32_t s0[32], s1[32];
+        tmem_ld32_nowait(tP, s0);
+        tmem_ld32_nowait(tP + 32, s1);
+        // V of slots outside hidden .. kv - 1 may hold anything (stale pages):
+        // 0 there, for 0 * NaN is not 0
         if (key0 + kAcKeys > k.kv || key0 < k.hid) {
           const int vp = pos + min(lag, k.nc) + c + min(c, max(0, k.nc - lag));
           if (!warp_wait(&kv_full[vp % NS], (vp / NS) & 1)) {
             ok = false;
             break;
           }
-          if (row < D) {
-            uint8_t* v = sKV + (vp % NS) * C::kStage + row * 128;
-#pragma unroll 1
-            for (int q = 0; q < 16; ++q) {
-              const int s0 = key0 + q * 8;
-              if (s0 + 8 <= k.kv && s0 >= k.hid) continue;
-              uint4* pv = reinterpret_cast<uint4*>(v + (q >> 3) * (D * 128) + (((q & 7) ^ (row & 7)) << 4));
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (s0 < k.kv && s0 + 8 > k.hid) {
-                x = *pv;
-                uint32_t* xe = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int sa = s0 + 2 * e;
-                  xe[e] &= ((sa < k.kv && sa >= k.hid) ? 0x0000FFFFu : 0u) |
-                           ((sa + 1 < k.kv && sa + 1 >= k.hid) ? 0xFFFF0000u : 0u);
-                }
-              }
-              *pv = x;
-            }
-          }
+          if (row < D) clear_outside(sKV + (vp % NS) * C::kStage + row * 128, row & 7, k.kv - key0, k.hid - key0);
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
+        tmem_wait_ld32(s0);
+        tmem_wait_ld32(s1);
+        if (live) {
+          if (__any_sync(0xffffffffu, key0 + kAcKeys > lim || key0 < lo_slot)) {
+            mask32(s0, lim - key0, lo_slot - key0);
+            mask32(s1, lim - key0 - 32, lo_slot - key0 - 32);
+          }
+          const float mx = max32(s1, max32(s0, -INFINITY));
+          // the reference maximum moves only past the headroom (or from -inf):
+          // P then stays below 2^8, and O is seldom rescaled
+          const bool move = mx > m + lazy || (m == -INFINITY && mx > -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? ex2((m - mx) * sl2) : 1.f;
+            if (move) m = mx;
+            l *= f;
+            if (c >= step) {  // once every product of the earlier pages is in O
+              if (!warp_wait(&pv_done[w], (ns - 2) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 16) {
+                float o[16];
+                tmem_ld16(tO + cc, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_st16_nowait(tO + cc, o);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m * sl2;
+          const uint64_t neg2 = pack2(neg, neg), sl22 = pack2(sl2, sl2);
+          uint32_t pk[32];
+          const float sum = exp_block<kAcPoly>(s0, sl22, neg2, pk);
+          l += sum + exp_block<kAcPoly>(s1, sl22, neg2, pk + 16);
+          tmem_st32_nowait(tP, pk);
+          tmem_wait_st();
+        }  // else no row of this warp is one of the item's: its P and O are never used
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        if (lane == 0) mbar_arrive(&p_full[w * 2 + buf]);
       }
       pos += 2 * k.nc;
       if (!ok) break;
-      // ---------------------------------------------- the item's rows
-      const int mine_nc = (k.nc - first + step - 1) / step;  // chunks of this warpgroup
-      if (mine_nc > 0) {
-        if (!warp_wait(&o_done[w], no & 1)) break;
-        ++no;
-      }
+      if (m == -INFINITY) l = 0.f;  // a row that saw nothing (masked scores may leave 2^-126 each)
+      if (k.nc > first && !warp_wait(&o_done[w], no++ & 1)) break;
       tc_fence_after();
       if (solo) {
         // both warpgroups hold the same rows over alternate chunks: each
@@ -697,39 +832,15 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const float f0 = k.slot < 0 ? a0 * inv : a0, f1 = k.slot < 0 ? a1 * inv : a1;
         constexpr int HD = D / 2;
 #pragma unroll 1
-        for (int cc = 0; cc < HD; cc += 32) {
+        for (int cc = 0; live && cc < HD; cc += 16) {
           const int col = w * HD + cc;
-          uint32_t x[32], y[32];
-          tmem_ld32_nowait(tl + kAcColO + col, x);
-          tmem_ld32_nowait(tl + kAcColO + D + col, y);
-          tmem_wait_ld32(x);
-          tmem_wait_ld32(y);
+          float x[16], y[16];
+          tmem_ld16(tl + kAcColO + col, x);
+          tmem_ld16(tl + kAcColO + D + col, y);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            // an accumulator that no chunk reached holds anything
-            const float u = h0 && a0 > 0.f ? __uint_as_float(x[j]) * f0 : 0.f;
-            const float v = h1 && a1 > 0.f ? __uint_as_float(y[j]) * f1 : 0.f;
-            x[j] = __float_as_uint(u + v);
-          }
-          if (k.slot < 0) {
-            if (valid) {
-              uint4* dst = reinterpret_cast<uint4*>(
-                  a.out + (static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh) * D + col);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint4 v4;
-                v4.x = pack_bf16(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]));
-                v4.y = pack_bf16(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]));
-                v4.z = pack_bf16(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]));
-                v4.w = pack_bf16(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7]));
-                dst[q] = v4;
-              }
-            }
-          } else if (valid) {
-            float* dst = ws.o + (static_cast<size_t>(cta * 2 + k.slot) * 2 * D + col) * 128 + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(x[j]);
-          }
+          for (int j = 0; j < 16; ++j)  // an accumulator that no chunk reached holds anything
+            x[j] = (h0 && a0 > 0.f ? x[j] * f0 : 0.f) + (h1 && a1 > 0.f ? y[j] * f1 : 0.f);
+          store_cols(k, tok, valid, 0, col, x);
         }
         if (w == 0 && valid) {
           if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + row] = make_float2(mm, lt);
@@ -742,30 +853,12 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float f = k.slot < 0 ? inv : 1.f;
 #pragma unroll 1
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t x[32];
-          tmem_ld32_nowait(tO + cc, x);
-          tmem_wait_ld32(x);
+        for (int cc = 0; live && cc < D; cc += 16) {
+          float x[16];
+          tmem_ld16(tO + cc, x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = k.nc > 0 && l > 0.f ? __float_as_uint(__uint_as_float(x[j]) * f) : 0u;
-          if (!valid) continue;
-          if (k.slot < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(
-                a.out + (static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh) * D + cc);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4 v4;
-              v4.x = pack_bf16(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]));
-              v4.y = pack_bf16(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]));
-              v4.z = pack_bf16(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]));
-              v4.w = pack_bf16(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7]));
-              dst[q] = v4;
-            }
-          } else {
-            float* dst = ws.o + ((static_cast<size_t>(cta * 2 + k.slot) * 2 + w) * D + cc) * 128 + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(x[j]);
-          }
+          for (int j = 0; j < 16; ++j) x[j] = k.nc > 0 && l > 0.f ? x[j] * f : 0.f;
+          store_cols(k, tok, valid, w, cc, x);
         }
         if (valid) {
           if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + w * 128 + row] = make_float2(m, l);
@@ -787,56 +880,52 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   }
 }
 
-// Rows of items that were cut: block (p, q) combines 32-row group q of the
-// item that CTA p began and others finished.  Partials are summed in CTA
-// order.  A warp takes D / 8 features, a lane a row.
-constexpr int kAmThreads = 256;
+// Rows of items that were cut: block (p, tile) combines the item that CTA p
+// began and others finished, its partials in CTA order.  A warp takes 32 rows
+// (a lane a row) and D / 8 features.
+constexpr int kAmThreads = 1024;
 template <int D>
 __global__ void __launch_bounds__(kAmThreads) attn_chunk_merge_kernel(const ChunkAttnArgs a, int P) {
   griddep_wait();
   const AcPart ws = ac_carve(a.workspace, P, D);
-  const int p0 = blockIdx.x;
-  const int* rec = ws.rec + p0 * 16;
-  const int kind = rec[0];
-  if (kind == 0) return;
-  const int tile = blockIdx.y >> 2, quarter = blockIdx.y & 3;
-  if (kind == 2 && tile > 0) return;
-  const int last = rec[1], row0 = rec[2], ntok = rec[3], g = rec[4];
+  const int p0 = blockIdx.x, tile = blockIdx.y;
+  const int4 r4 = *reinterpret_cast<const int4*>(ws.rec + p0 * 16);  // kind, last CTA, first row, rows
+  const int g = ws.rec[p0 * 16 + 4];
+  if (r4.x == 0 || (r4.x == 2 && tile > 0)) return;
+  const int last = r4.y, row0 = r4.z, ntok = r4.w;
   const int G = a.Hq / a.Hkv, tpt = 128 / G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = quarter * 32 + lane;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, part = warp >> 2;
   const int rt = row / G, rh = row - rt * G, tok = tile * tpt + rt;
-  const bool valid = rt < tpt && tok < ntok;
-  if (!__any_sync(0xffffffffu, valid)) return;
+  if (rt >= tpt || tok >= ntok) return;
   constexpr int F = D / 8;
   float acc[F];
 #pragma unroll
   for (int j = 0; j < F; ++j) acc[j] = 0.f;
   float m = -INFINITY, l = 0.f;
   auto slot_of = [&](int p) { return (p * 2 + (p == p0 ? 1 : 0)) * 2 + tile; };
-  if (valid) {
-    for (int p = p0; p <= last; ++p) m = fmaxf(m, ws.ml[slot_of(p) * 128 + row].x);
-    if (m > -INFINITY) {
-#pragma unroll 2
-      for (int p = p0; p <= last; ++p) {
-        const float2 ml = ws.ml[slot_of(p) * 128 + row];
-        if (ml.x == -INFINITY) continue;
-        const float e = ex2((ml.x - m) * a.scale_log2);
-        l += e * ml.y;
-        const float* o = ws.o + (static_cast<size_t>(slot_of(p)) * D + warp * F) * 128 + row;
+#pragma unroll 4
+  for (int p = p0; p <= last; ++p) m = fmaxf(m, ws.ml[slot_of(p) * 128 + row].x);
+  if (m > -INFINITY) {
+#pragma unroll 4
+    for (int p = p0; p <= last; ++p) {
+      const float2 ml = ws.ml[slot_of(p) * 128 + row];
+      const float* o = ws.o + (static_cast<size_t>(slot_of(p)) * D + part * F) * 128 + row;
+      // a part that saw nothing of the row holds zeros
+      const float e = ml.x == -INFINITY ? 0.f : ex2((ml.x - m) * a.scale_log2);
+      l += e * ml.y;
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[j] += e * o[j * 128];
-      }
+      for (int j = 0; j < F; ++j) acc[j] += e * o[j * 128];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
-    uint32_t pk[F / 2];
-#pragma unroll
-    for (int j = 0; j < F / 2; ++j) pk[j] = pack_bf16(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-    uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + warp * F);
-#pragma unroll
-    for (int q = 0; q < F / 8; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-    if (a.lse && warp == 0) a.lse[at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
+  uint32_t pk[F / 2];
+#pragma unroll
+  for (int j = 0; j < F / 2; ++j) pk[j] = pack_bf16(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + part * F);
+#pragma unroll
+  for (int q = 0; q < F / 8; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+  if (a.lse && part == 0) a.lse[at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 namespace {
@@ -850,7 +939,7 @@ cudaError_t run_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensor
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(P, 8);
+  cfg.gridDim = dim3(P, 2);
   cfg.blockDim = dim3(kAmThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

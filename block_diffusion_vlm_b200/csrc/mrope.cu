@@ -10,12 +10,15 @@
 // and sine of the reduced angle, the products and the sum are fp32; one
 // rounding at the store.
 //
-// Bound: HBM (each element read once, written once).  A row's (cos, sin)
-// table is shared by all its heads, so a block takes a tile of rows, builds
-// their table once in shared memory and streams the heads past it in 16-byte
-// pieces.  V is stored feature-major in its page: the block turns a 32-row
-// tile through shared memory, so that one warp writes 32 consecutive slots of
-// a feature.
+// Bound: HBM (each element read once, written once).  A warp owns a row: it
+// sends out the loads of its first kMrBatch pieces per lane (16 bytes of each
+// half), forms the row's (cos, sin) while they are on their way, and then
+// turns and stores.  No block-wide step after the first, so that the warps of
+// an SM are in different phases and the loads never pause (a block building a
+// table for 32 rows first reached half the bandwidth).  V is stored
+// feature-major in its page: separate blocks turn 64-row tiles of a value
+// head through shared memory; eight rows on eight aligned slots of a page
+// leave as 16-byte pieces.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -23,7 +26,9 @@ namespace dvlm {
 
 namespace {
 constexpr int kMrThreads = 256;
-constexpr int kMrRows = 32;                 // rows per block
+constexpr int kMrWarps = kMrThreads / 32;
+constexpr int kMrBatch = 4;                 // pieces in flight per lane
+constexpr int kMrVRows = 64;                // rows of a value tile
 constexpr double kInv2Pi = 0.15915494309189533577;
 
 // Axis of frequency j: sections in order (axis 0's frequencies first), or
@@ -39,23 +44,38 @@ __device__ __forceinline__ int mrope_axis(const MropeAxes& ax, int j) {
   return a;
 }
 
-// (cos, sin) of rows row0 .. row0 + n - 1 into cs[row][half]; freq[half] (in
-// turns per position) is scratch.
-__device__ __forceinline__ void mrope_table(const MropeAxes& ax, int row0, int n, int n_rows, double* freq,
-                                            uint8_t* axis, float2* cs) {
-  const int half = ax.rot / 2;
-  for (int j = threadIdx.x; j < half; j += kMrThreads) {
-    freq[j] = exp2(-2.0 * j / ax.rot * ax.log2_base) * kInv2Pi;
-    axis[j] = static_cast<uint8_t>(mrope_axis(ax, j));
+// Shared memory of a block: freq [half] (turns per position, fp64), the axes'
+// position row offsets [half], then a (cos, sin) row per warp.
+struct MrSmem {
+  double* freq;
+  float2* cs;  // this warp's
+  int* axis;
+};
+__device__ __forceinline__ MrSmem mr_carve(uint8_t* smem, int half, int warp) {
+  MrSmem s;
+  s.freq = reinterpret_cast<double*>(smem);
+  s.cs = reinterpret_cast<float2*>(s.freq + half) + warp * half;
+  s.axis = reinterpret_cast<int*>(reinterpret_cast<float2*>(s.freq + half) + kMrWarps * half);
+  return s;
+}
+inline size_t mr_smem(int half) { return static_cast<size_t>(half) * (8 + 8 * kMrWarps + 4); }
+
+__device__ __forceinline__ void mr_freqs(const MropeAxes& ax, const MrSmem& s) {
+  for (int j = threadIdx.x; j < ax.rot / 2; j += kMrThreads) {
+    s.freq[j] = exp2(-2.0 * j / ax.rot * ax.log2_base) * kInv2Pi;
+    s.axis[j] = mrope_axis(ax, j);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n * half; i += kMrThreads) {
-    const int r = i / half, j = i - r * half;
-    const double t = ax.pos[static_cast<size_t>(axis[j]) * n_rows + row0 + r] * freq[j];
-    float s, c;
-    sincospif(2.0f * static_cast<float>(t - rint(t)), &s, &c);
-    cs[i] = make_float2(c, s);
+}
+// (cos, sin) of a row into the warp's table.
+__device__ __forceinline__ void mr_angles(const MropeAxes& ax, const MrSmem& s, int row, int n_rows, int lane) {
+  for (int j = lane; j < ax.rot / 2; j += 32) {
+    const double t = ax.pos[static_cast<size_t>(s.axis[j]) * n_rows + row] * s.freq[j];
+    float sn, c;
+    sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &c);
+    s.cs[j] = make_float2(c, sn);
   }
+  __syncwarp();
 }
 
 template <typename T, int N>
@@ -69,134 +89,216 @@ __device__ __forceinline__ void from_f(float x, bf16& y) { y = __float2bfloat16_
 
 // (explicit multiply-adds: every piece width rounds alike)
 template <typename T, int N>
-__device__ __forceinline__ void turn(const Vec<T, N>& a, const Vec<T, N>& b, const float2* cs, Vec<T, N>& ya,
-                                     Vec<T, N>& yb) {
+__device__ __forceinline__ void turn(Vec<T, N>& a, Vec<T, N>& b, const float2* cs) {
 #pragma unroll
   for (int e = 0; e < N; ++e) {
+    const float2 w = cs[e];
     const float x = to_f(a.v[e]), y = to_f(b.v[e]);
-    from_f(__fmaf_rn(x, cs[e].x, -__fmul_rn(y, cs[e].y)), ya.v[e]);
-    from_f(__fmaf_rn(y, cs[e].x, __fmul_rn(x, cs[e].y)), yb.v[e]);
+    from_f(__fmaf_rn(x, w.x, -__fmul_rn(y, w.y)), a.v[e]);
+    from_f(__fmaf_rn(y, w.x, __fmul_rn(x, w.y)), b.v[e]);
+  }
+}
+
+// Pieces of a row of `heads` heads of D: piece i is (head i / np, pair piece
+// i % np), np = half / N; walked by a lane in steps of 32 without dividing.
+struct Walk {
+  int h, p, np, dh, dp;
+  __device__ __forceinline__ Walk(int lane, int np_) : np(np_) {
+    h = lane / np;
+    p = lane - h * np;
+    dh = 32 / np;
+    dp = 32 - dh * np;
+  }
+  __device__ __forceinline__ void next() {
+    h += dh;
+    p += dp;
+    if (p >= np) {
+      p -= np;
+      ++h;
+    }
+  }
+};
+
+// One row: heads h of src at h * D turned into dst(h).
+template <typename T, int N, typename Dst>
+__device__ __forceinline__ void turn_row(const T* src, const Dst& dst, int heads, int D, const MropeAxes& ax,
+                                         const MrSmem& s, int row, int n_rows, int lane, const Walk& first) {
+  using V = Vec<T, N>;
+  const int half = ax.rot / 2;
+  Walk rd = first, wr = first;
+  bool have_angles = false;
+  while (__any_sync(0xffffffffu, rd.h < heads)) {
+    V a[kMrBatch], b[kMrBatch];
+#pragma unroll
+    for (int u = 0; u < kMrBatch; ++u) {
+      if (rd.h < heads) {
+        const T* x = src + rd.h * D + rd.p * N;
+        a[u] = *reinterpret_cast<const V*>(x);
+        b[u] = *reinterpret_cast<const V*>(x + half);
+      }
+      rd.next();
+    }
+    if (!have_angles) mr_angles(ax, s, row, n_rows, lane);
+    have_angles = true;
+#pragma unroll
+    for (int u = 0; u < kMrBatch; ++u) {
+      if (wr.h < heads) {
+        turn(a[u], b[u], s.cs + wr.p * N);
+        T* y = dst(wr.h) + wr.p * N;
+        *reinterpret_cast<V*>(y) = a[u];
+        *reinterpret_cast<V*>(y + half) = b[u];
+      }
+      wr.next();
+    }
+  }
+  __syncwarp();  // the table is read before the next row's
+}
+// The elements from rot on of a row's heads, copied.
+template <typename T, int N, typename Dst>
+__device__ __forceinline__ void copy_tails(const T* src, const Dst& dst, int heads, int D, int rot, int lane) {
+  using V = Vec<T, N>;
+  const int nt = (D - rot) / N;
+  for (int i = lane; i < heads * nt; i += 32) {
+    const int h = i / nt, at = rot + (i - h * nt) * N;
+    *reinterpret_cast<V*>(dst(h) + at) = *reinterpret_cast<const V*>(src + h * D + at);
   }
 }
 }  // namespace
 
-// out[r, h, :] = x[r, h, :] turned (N elements of a half per piece).  grid:
-// (row tiles, head groups).
+// out[r, h, :] = x[r, h, :] turned.  Units: (row, group of heads).
 template <typename T, int N>
 __global__ void __launch_bounds__(kMrThreads) mrope_rows_kernel(const T* x, T* out, long long x_ld, long long out_ld,
-                                                                int n_rows, int n_heads, int D, const MropeAxes ax) {
+                                                                int n_rows, int n_heads, int D, int groups,
+                                                                const MropeAxes ax) {
   extern __shared__ __align__(16) uint8_t smem[];
-  const int half = ax.rot / 2, row0 = blockIdx.x * kMrRows, n = min(kMrRows, n_rows - row0);
-  double* freq = reinterpret_cast<double*>(smem);
-  float2* cs = reinterpret_cast<float2*>(freq + half);
-  uint8_t* axis = reinterpret_cast<uint8_t*>(cs + kMrRows * half);
-  const int hpg = (n_heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * hpg, hn = min(hpg, n_heads - h0);
-  mrope_table(ax, row0, n, n_rows, freq, axis, cs);
-  __syncthreads();
-  if (hn <= 0) return;
-  const int np = half / N, tail = x == out ? 0 : (D - ax.rot) / N;  // pieces: turned pairs, then copies
-  const int per_head = np + tail, per_row = hn * per_head;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n * per_row; i += kMrThreads) {
-    const int r = i / per_row, k = i - r * per_row, h = k / per_head, p = k - h * per_head;
-    const T* src = x + (row0 + r) * x_ld + static_cast<long long>(h0 + h) * D;
-    T* dst = out + (row0 + r) * out_ld + static_cast<long long>(h0 + h) * D;
-    using V = Vec<T, N>;
-    if (p < np) {
-      const V a = *reinterpret_cast<const V*>(src + p * N), b = *reinterpret_cast<const V*>(src + half + p * N);
-      V ya, yb;
-      turn(a, b, cs + r * half + p * N, ya, yb);
-      *reinterpret_cast<V*>(dst + p * N) = ya;
-      *reinterpret_cast<V*>(dst + half + p * N) = yb;
-    } else {
-      const int at = ax.rot + (p - np) * N;
-      *reinterpret_cast<V*>(dst + at) = *reinterpret_cast<const V*>(src + at);
-    }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MrSmem s = mr_carve(smem, ax.rot / 2, warp);
+  mr_freqs(ax, s);
+  const Walk first(lane, ax.rot / 2 / N);
+  const int hpg = (n_heads + groups - 1) / groups;
+  for (long long i = static_cast<long long>(blockIdx.x) * kMrWarps + warp; i < static_cast<long long>(n_rows) * groups;
+       i += static_cast<long long>(gridDim.x) * kMrWarps) {
+    const int row = static_cast<int>(i / groups), h0 = static_cast<int>(i - static_cast<long long>(row) * groups) * hpg;
+    const int heads = min(hpg, n_heads - h0);
+    if (heads <= 0) continue;
+    const T* src = x + row * x_ld + static_cast<long long>(h0) * D;
+    T* dst = out + row * out_ld + static_cast<long long>(h0) * D;
+    auto at = [&](int h) { return dst + static_cast<long long>(h) * D; };
+    turn_row<T, N>(src, at, heads, D, ax, s, row, n_rows, lane, first);
+    if (ax.rot < D && x != out) copy_tails<T, N>(src, at, heads, D, ax.rot, lane);
   }
 }
 
 // One row of qkv = [Hq query heads | Hkv key heads | Hkv value heads]: queries
 // turned into q_out, keys turned into their page slot, values into their
 // feature-major page.  A row with slot -1 is padding: nothing is written.
-// grid: (row tiles, groups of the Hq + 2 Hkv heads).
+// Blocks 0 .. v_blocks - 1 take the value tiles (64 rows of one head), the
+// others (row, head group) units of the queries and keys.
 template <int D, int N>
-__global__ void __launch_bounds__(kMrThreads) mrope_append_kernel(const MropeAppendArgs a) {
+__global__ void __launch_bounds__(kMrThreads) mrope_append_kernel(const MropeAppendArgs a, int v_blocks, int groups) {
   extern __shared__ __align__(16) uint8_t smem[];
-  const int half = a.ax.rot / 2, row0 = blockIdx.x * kMrRows, n = min(kMrRows, a.n_rows - row0);
-  bf16* vt = reinterpret_cast<bf16*>(smem);                       // [kMrRows][D + 2] one value head
-  constexpr int kVtLd = D + 2;
-  double* freq = reinterpret_cast<double*>(smem + kMrRows * kVtLd * 2);
-  float2* cs = reinterpret_cast<float2*>(freq + half);
-  int* slot = reinterpret_cast<int*>(cs + kMrRows * half);
-  uint8_t* axis = reinterpret_cast<uint8_t*>(slot + kMrRows);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int hpg = (heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * hpg, h1 = min(heads, h0 + hpg);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_slots = a.n_pages * 64;
-  if (threadIdx.x < kMrRows) {
-    int sl = threadIdx.x < n ? a.slot_map[row0 + threadIdx.x] : -1;
-    if (sl < -1 || sl >= n_slots) {
-      record_error(a.status, DVLM_ERR_BOUNDS);
-      sl = -1;
+  auto slot_of = [&](int row) {
+    const int sl = a.slot_map[row];
+    if (sl >= -1 && sl < n_slots) return sl;
+    record_error(a.status, DVLM_ERR_BOUNDS);
+    return -1;
+  };
+  if (static_cast<int>(blockIdx.x) >= v_blocks) {
+    const MrSmem s = mr_carve(smem, a.ax.rot / 2, warp);
+    mr_freqs(a.ax, s);
+    const Walk first(lane, a.ax.rot / 2 / N);
+    const int heads = a.Hq + a.Hkv, hpg = (heads + groups - 1) / groups;
+    const long long n_units = static_cast<long long>(a.n_rows) * groups;
+    const long long n_warps = static_cast<long long>(gridDim.x - v_blocks) * kMrWarps;
+    for (long long i = static_cast<long long>(blockIdx.x - v_blocks) * kMrWarps + warp; i < n_units; i += n_warps) {
+      const int row = static_cast<int>(i / groups);
+      const int h0 = static_cast<int>(i - static_cast<long long>(row) * groups) * hpg, hn = min(hpg, heads - h0);
+      const int sl = slot_of(row);
+      if (sl < 0 || hn <= 0) continue;
+      const bf16* src = a.qkv + row * a.qkv_ld + h0 * D;
+      bf16* q = a.q_out + (static_cast<size_t>(row) * a.Hq + h0) * D;
+      bf16* k = a.k_pages + ((static_cast<size_t>(sl >> 6) * a.Hkv + h0) * 64 + (sl & 63)) * D -
+                static_cast<size_t>(a.Hq) * 64 * D;
+      auto at = [&](int h) { return h0 + h < a.Hq ? q + h * D : k + static_cast<size_t>(h) * 64 * D; };
+      turn_row<bf16, N>(src, at, hn, D, a.ax, s, row, a.n_rows, lane, first);
+      if (a.ax.rot < D) copy_tails<bf16, N>(src, at, hn, D, a.ax.rot, lane);
     }
-    slot[threadIdx.x] = sl;
+    return;
   }
-  const int hr = min(h1, a.Hq + a.Hkv);  // heads h0 .. hr - 1 are turned, hr .. h1 - 1 are values
-  if (h0 < hr) mrope_table(a.ax, row0, n, a.n_rows, freq, axis, cs);
+  // value tile: rows row0 .. of head g, [row][D + 2] in shared memory
+  constexpr int kLd = D + 2;
+  bf16* vt = reinterpret_cast<bf16*>(smem);
+  int* slot = reinterpret_cast<int*>(vt + kMrVRows * kLd);
+  const int row0 = static_cast<int>(blockIdx.x) / a.Hkv * kMrVRows, g = static_cast<int>(blockIdx.x) % a.Hkv;
+  const int n = min(kMrVRows, a.n_rows - row0);
+  const bf16* src = a.qkv + row0 * a.qkv_ld + (a.Hq + a.Hkv + g) * D;
+  if (threadIdx.x < kMrVRows) slot[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? slot_of(row0 + threadIdx.x) : -1;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n * (D / 8); i += kMrThreads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const uint4 v = *reinterpret_cast<const uint4*>(src + r * a.qkv_ld + c * 8);
+    uint32_t* d = reinterpret_cast<uint32_t*>(vt + r * kLd + c * 8);
+    d[0] = v.x;
+    d[1] = v.y;
+    d[2] = v.z;
+    d[3] = v.w;
+  }
   __syncthreads();
-
-  using V = Vec<bf16, N>;
-  const int np = half / N, per_head = np + (D - a.ax.rot) / N, per_row = max(hr - h0, 0) * per_head;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n * per_row; i += kMrThreads) {
-    const int r = i / per_row, k = i - r * per_row, hh = k / per_head, p = k - hh * per_head, h = h0 + hh;
+  auto put = [&](int r, int d) {
     const int sl = slot[r];
-    if (sl < 0) continue;
-    const bf16* src = a.qkv + (row0 + r) * a.qkv_ld + h * D;
-    bf16* dst = h < a.Hq ? a.q_out + (static_cast<size_t>(row0 + r) * a.Hq + h) * D
-                         : a.k_pages + ((static_cast<size_t>(sl >> 6) * a.Hkv + (h - a.Hq)) * 64 + (sl & 63)) * D;
-    if (p < np) {
-      const V x = *reinterpret_cast<const V*>(src + p * N), y = *reinterpret_cast<const V*>(src + half + p * N);
-      V ya, yb;
-      turn(x, y, cs + r * half + p * N, ya, yb);
-      *reinterpret_cast<V*>(dst + p * N) = ya;
-      *reinterpret_cast<V*>(dst + half + p * N) = yb;
+    if (sl >= 0) a.v_pages[((static_cast<size_t>(sl >> 6) * a.Hkv + g) * D + d) * 64 + (sl & 63)] = vt[r * kLd + d];
+  };
+  // rows r0, r0 + 8, ... lead pieces of eight, r0 where the first row's slots
+  // come to a multiple of eight; pieces whose slots do not follow one another,
+  // and the rows before r0, go one by one
+  const int r0 = slot[0] >= 0 ? min(n, (8 - (slot[0] & 7)) & 7) : 0;
+  for (int i = threadIdx.x; i < r0 * D; i += kMrThreads) put(i / D, i % D);
+  for (int i = threadIdx.x; i < kMrVRows / 8 * D; i += kMrThreads) {
+    // lanes: eight pieces next to one another (a 128-byte line of a page's feature row), then features
+    const int d = i >> 3, lo = r0 + (i & 7) * 8, hi = min(n, lo + 8);
+    if (lo >= hi) continue;
+    const int s0 = slot[lo];
+    bool run = hi - lo == 8 && s0 >= 0 && (s0 & 7) == 0;
+    if (run) {
+#pragma unroll
+      for (int e = 1; e < 8; ++e) run &= slot[lo + e] == s0 + e;
+    }
+    if (run) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = *reinterpret_cast<const uint16_t*>(vt + (lo + 2 * e) * kLd + d);
+        const uint32_t y = *reinterpret_cast<const uint16_t*>(vt + (lo + 2 * e + 1) * kLd + d);
+        w[e] = x | (y << 16);
+      }
+      *reinterpret_cast<uint4*>(a.v_pages + ((static_cast<size_t>(s0 >> 6) * a.Hkv + g) * D + d) * 64 + (s0 & 63)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-      const int at = a.ax.rot + (p - np) * N;
-      *reinterpret_cast<V*>(dst + at) = *reinterpret_cast<const V*>(src + at);
-    }
-  }
-  for (int h = max(h0, a.Hq + a.Hkv); h < h1; ++h) {
-    const int g = h - a.Hq - a.Hkv;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * (D / 2); i += kMrThreads) {
-      const int r = i / (D / 2), c = i - r * (D / 2);
-      *reinterpret_cast<uint32_t*>(vt + r * kVtLd + 2 * c) =
-          *reinterpret_cast<const uint32_t*>(a.qkv + (row0 + r) * a.qkv_ld + h * D + 2 * c);
-    }
-    __syncthreads();
-    const int r = threadIdx.x & 31, sl = slot[r];
-    if (sl >= 0) {
-      bf16* page = a.v_pages + (static_cast<size_t>(sl >> 6) * a.Hkv + g) * D * 64 + (sl & 63);
-      for (int d = threadIdx.x >> 5; d < D; d += kMrThreads / 32) page[d * 64] = vt[r * kVtLd + d];
+      for (int r = lo; r < hi; ++r) put(r, d);
     }
   }
 }
 
 namespace {
-// Head groups (grid y): one group where the row tiles alone fill the GPU
-// (the angle table is then built once a row), else as many as give every SM a
-// few blocks, down to one head a block.
-int head_groups(int row_tiles, int heads) {
-  const int want = 4 * 148 / row_tiles;
+// Head groups per row: one where the rows alone fill the GPU's warps, else as
+// many as give each SM a few warps of work, down to one head.
+int head_groups(int n_rows, int heads) {
+  const int want = 148 * 16 / n_rows;
   return want < 1 ? 1 : (want > heads ? heads : want);
+}
+// Blocks for n_units warps of work, at most what the SMs hold at once.
+int unit_blocks(long long n_units) {
+  const long long b = (n_units + kMrWarps - 1) / kMrWarps, most = static_cast<long long>(device_sm_count()) * 8;
+  return static_cast<int>(b < most ? b : most);
 }
 template <typename T, int N>
 cudaError_t run_rows(const T* x, T* out, long long x_ld, long long out_ld, int n_rows, int n_heads, int D,
                      const MropeAxes& ax, cudaStream_t s) {
-  const int half = ax.rot / 2, tiles = (n_rows + kMrRows - 1) / kMrRows;
-  const size_t sm = static_cast<size_t>(half) * (8 + 1) + static_cast<size_t>(kMrRows) * half * 8;
-  mrope_rows_kernel<T, N><<<dim3(tiles, head_groups(tiles, n_heads)), kMrThreads, sm, s>>>(x, out, x_ld, out_ld, n_rows,
-                                                                                        n_heads, D, ax);
+  const int groups = head_groups(n_rows, n_heads);
+  mrope_rows_kernel<T, N><<<unit_blocks(static_cast<long long>(n_rows) * groups), kMrThreads, mr_smem(ax.rot / 2), s>>>(
+      x, out, x_ld, out_ld, n_rows, n_heads, D, groups, ax);
   return cudaGetLastError();
 }
 template <typename T>
@@ -205,7 +307,7 @@ cudaError_t rows_by_width(const T* x, T* out, long long x_ld, long long out_ld, 
   // widest piece that divides both halves, the head and the strides and keeps every access aligned
   auto fits = [&](int n) {
     const long long b = n * static_cast<long long>(sizeof(T));
-    return (ax.rot / 2) % n == 0 && D % n == 0 && ax.rot % n == 0 && x_ld % n == 0 && out_ld % n == 0 &&
+    return (ax.rot / 2) % n == 0 && D % n == 0 && x_ld % n == 0 && out_ld % n == 0 &&
            reinterpret_cast<uintptr_t>(x) % b == 0 && reinterpret_cast<uintptr_t>(out) % b == 0;
   };
   constexpr int kMax = 16 / sizeof(T);
@@ -215,13 +317,14 @@ cudaError_t rows_by_width(const T* x, T* out, long long x_ld, long long out_ld, 
 }
 template <int D>
 cudaError_t run_append(const MropeAppendArgs& a, cudaStream_t s) {
-  const int half = a.ax.rot / 2, tiles = (a.n_rows + kMrRows - 1) / kMrRows;
-  const size_t sm = kMrRows * (D + 2) * 2 + static_cast<size_t>(half) * (8 + 1) +
-                    static_cast<size_t>(kMrRows) * half * 8 + kMrRows * 4;
-  const dim3 grid(tiles, head_groups(tiles, a.Hq + 2 * a.Hkv));
+  const int groups = head_groups(a.n_rows, a.Hq + a.Hkv);
+  const int v_blocks = (a.n_rows + kMrVRows - 1) / kMrVRows * a.Hkv;
+  const size_t sv = kMrVRows * (D + 2) * 2 + kMrVRows * 4, sr = mr_smem(a.ax.rot / 2);
+  const int blocks = v_blocks + unit_blocks(static_cast<long long>(a.n_rows) * groups);
+  const size_t sm = sv > sr ? sv : sr;
   // 16-byte pieces wherever the halves allow them
-  if (half % 8 == 0) mrope_append_kernel<D, 8><<<grid, kMrThreads, sm, s>>>(a);
-  else mrope_append_kernel<D, 1><<<grid, kMrThreads, sm, s>>>(a);
+  if (a.ax.rot % 16 == 0) mrope_append_kernel<D, 8><<<blocks, kMrThreads, sm, s>>>(a, v_blocks, groups);
+  else mrope_append_kernel<D, 1><<<blocks, kMrThreads, sm, s>>>(a, v_blocks, groups);
   return cudaGetLastError();
 }
 }  // namespace
