@@ -437,7 +437,8 @@ dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int
       n_pages > kMaxPages || max_rows < 1)
     return DVLM_ERR_SHAPE;
   PagePlanArgs a{cache_len, new_len, block_table, free_pages, free_count, n_batch, max_pages, n_pages, max_rows,
-                 kv_len, cu_rows, slot_map, free_count_out, dev_status};
+                 kv_len, cu_rows, slot_map, free_count_out, kv_len == cache_len || free_count_out == free_count,
+                 dev_status};
   return cuda_status(launch_page_plan(a, cs(stream)));
 }
 

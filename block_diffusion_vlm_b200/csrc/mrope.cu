@@ -27,7 +27,8 @@ namespace dvlm {
 namespace {
 constexpr int kMrThreads = 256;
 constexpr int kMrWarps = kMrThreads / 32;
-constexpr int kMrBatch = 4;                 // pieces in flight per lane
+constexpr int kMrBlocks = 4;                // resident blocks per SM (64 registers a thread)
+constexpr int kMrBatch = 3;                 // pieces in flight per lane
 constexpr int kMrVRows = 64;                // rows of a value tile
 constexpr double kInv2Pi = 0.15915494309189533577;
 
@@ -44,21 +45,24 @@ __device__ __forceinline__ int mrope_axis(const MropeAxes& ax, int j) {
   return a;
 }
 
-// Shared memory of a block: freq [half] (turns per position, fp64), the axes'
-// position row offsets [half], then a (cos, sin) row per warp.
+// Shared memory of a block: freq [half] (turns per position, fp64), the axis
+// of each frequency, then a table of cosines and sines per warp, laid out for
+// pieces of N elements: element e of piece p at pair slot (e / 2) * np + p as
+// (cos, cos', sin, sin') of elements e and e + 1, so that the lanes of a head
+// read consecutive 16 bytes (N = 1: (cos, sin) of element p).
 struct MrSmem {
   double* freq;
-  float2* cs;  // this warp's
+  float* cs;  // this warp's
   int* axis;
 };
 __device__ __forceinline__ MrSmem mr_carve(uint8_t* smem, int half, int warp) {
   MrSmem s;
-  s.freq = reinterpret_cast<double*>(smem);
-  s.cs = reinterpret_cast<float2*>(s.freq + half) + warp * half;
-  s.axis = reinterpret_cast<int*>(reinterpret_cast<float2*>(s.freq + half) + kMrWarps * half);
+  s.cs = reinterpret_cast<float*>(smem) + warp * ((2 * half + 3) & ~3);
+  s.freq = reinterpret_cast<double*>(reinterpret_cast<float*>(smem) + kMrWarps * ((2 * half + 3) & ~3));
+  s.axis = reinterpret_cast<int*>(s.freq + half);
   return s;
 }
-inline size_t mr_smem(int half) { return static_cast<size_t>(half) * (8 + 8 * kMrWarps + 4); }
+inline size_t mr_smem(int half) { return static_cast<size_t>(kMrWarps) * ((2 * half + 3) & ~3) * 4 + half * 12; }
 
 __device__ __forceinline__ void mr_freqs(const MropeAxes& ax, const MrSmem& s) {
   for (int j = threadIdx.x; j < ax.rot / 2; j += kMrThreads) {
@@ -67,13 +71,21 @@ __device__ __forceinline__ void mr_freqs(const MropeAxes& ax, const MrSmem& s) {
   }
   __syncthreads();
 }
-// (cos, sin) of a row into the warp's table.
-__device__ __forceinline__ void mr_angles(const MropeAxes& ax, const MrSmem& s, int row, int n_rows, int lane) {
+// The table of a row.
+template <int N>
+__device__ __forceinline__ void mr_angles(const MropeAxes& ax, const MrSmem& s, int row, int n_rows, int np, int lane) {
   for (int j = lane; j < ax.rot / 2; j += 32) {
     const double t = ax.pos[static_cast<size_t>(s.axis[j]) * n_rows + row] * s.freq[j];
     float sn, c;
     sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &c);
-    s.cs[j] = make_float2(c, sn);
+    if constexpr (N == 1) {
+      s.cs[2 * j] = c;
+      s.cs[2 * j + 1] = sn;
+    } else {
+      float* d = s.cs + ((j % N) / 2 * np + j / N) * 4 + (j & 1);
+      d[0] = c;
+      d[2] = sn;
+    }
   }
   __syncwarp();
 }
@@ -82,6 +94,27 @@ template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
   T v[N];
 };
+// Two neighbouring elements as packed fp32, and back.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t widen2(const float* v) { return pack_f2(v[0], v[1]); }
+__device__ __forceinline__ uint64_t widen2(const bf16* v) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(v);
+  return pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void narrow2(uint64_t x, float* v) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(x));
+}
+__device__ __forceinline__ void narrow2(uint64_t x, bf16* v) {
+  float a, b;
+  uint32_t w;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  *reinterpret_cast<uint32_t*>(v) = w;
+}
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float x, float& y) { y = x; }
@@ -89,13 +122,25 @@ __device__ __forceinline__ void from_f(float x, bf16& y) { y = __float2bfloat16_
 
 // (explicit multiply-adds: every piece width rounds alike)
 template <typename T, int N>
-__device__ __forceinline__ void turn(Vec<T, N>& a, Vec<T, N>& b, const float2* cs) {
+__device__ __forceinline__ void turn(Vec<T, N>& a, Vec<T, N>& b, const float* cs, int p, int np) {
+  if constexpr (N == 1) {
+    const float c = cs[2 * p], s = cs[2 * p + 1], x = to_f(a.v[0]), y = to_f(b.v[0]);
+    from_f(__fmaf_rn(x, c, -__fmul_rn(y, s)), a.v[0]);
+    from_f(__fmaf_rn(y, c, __fmul_rn(x, s)), b.v[0]);
+  } else {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float2 w = cs[e];
-    const float x = to_f(a.v[e]), y = to_f(b.v[e]);
-    from_f(__fmaf_rn(x, w.x, -__fmul_rn(y, w.y)), a.v[e]);
-    from_f(__fmaf_rn(y, w.x, __fmul_rn(x, w.y)), b.v[e]);
+    for (int e = 0; e < N; e += 2) {
+      const float4 w = *reinterpret_cast<const float4*>(cs + ((e / 2) * np + p) * 4);
+      const uint64_t c = pack_f2(w.x, w.y), s = pack_f2(w.z, w.w), ns = pack_f2(-w.z, -w.w);
+      const uint64_t x = widen2(a.v + e), y = widen2(b.v + e);
+      uint64_t u, v;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(u) : "l"(y), "l"(ns));
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(s));
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(u) : "l"(x), "l"(c), "l"(u));
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(y), "l"(c), "l"(v));
+      narrow2(u, a.v + e);
+      narrow2(v, b.v + e);
+    }
   }
 }
 
@@ -119,6 +164,11 @@ struct Walk {
   }
 };
 
+// Row of unit i (more than one group of heads only where rows are few).
+__device__ __forceinline__ int unit_row(long long i, int groups) {
+  return groups == 1 ? static_cast<int>(i) : static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(groups));
+}
+
 // One row: heads h of src at h * D turned into dst(h).
 template <typename T, int N, typename Dst>
 __device__ __forceinline__ void turn_row(const T* src, const Dst& dst, int heads, int D, const MropeAxes& ax,
@@ -138,12 +188,12 @@ __device__ __forceinline__ void turn_row(const T* src, const Dst& dst, int heads
       }
       rd.next();
     }
-    if (!have_angles) mr_angles(ax, s, row, n_rows, lane);
+    if (!have_angles) mr_angles<N>(ax, s, row, n_rows, first.np, lane);
     have_angles = true;
 #pragma unroll
     for (int u = 0; u < kMrBatch; ++u) {
       if (wr.h < heads) {
-        turn(a[u], b[u], s.cs + wr.p * N);
+        turn(a[u], b[u], s.cs, wr.p, first.np);
         T* y = dst(wr.h) + wr.p * N;
         *reinterpret_cast<V*>(y) = a[u];
         *reinterpret_cast<V*>(y + half) = b[u];
@@ -167,7 +217,7 @@ __device__ __forceinline__ void copy_tails(const T* src, const Dst& dst, int hea
 
 // out[r, h, :] = x[r, h, :] turned.  Units: (row, group of heads).
 template <typename T, int N>
-__global__ void __launch_bounds__(kMrThreads) mrope_rows_kernel(const T* x, T* out, long long x_ld, long long out_ld,
+__global__ void __launch_bounds__(kMrThreads, kMrBlocks) mrope_rows_kernel(const T* x, T* out, long long x_ld, long long out_ld,
                                                                 int n_rows, int n_heads, int D, int groups,
                                                                 const MropeAxes ax) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -178,7 +228,7 @@ __global__ void __launch_bounds__(kMrThreads) mrope_rows_kernel(const T* x, T* o
   const int hpg = (n_heads + groups - 1) / groups;
   for (long long i = static_cast<long long>(blockIdx.x) * kMrWarps + warp; i < static_cast<long long>(n_rows) * groups;
        i += static_cast<long long>(gridDim.x) * kMrWarps) {
-    const int row = static_cast<int>(i / groups), h0 = static_cast<int>(i - static_cast<long long>(row) * groups) * hpg;
+    const int row = unit_row(i, groups), h0 = static_cast<int>(i - static_cast<long long>(row) * groups) * hpg;
     const int heads = min(hpg, n_heads - h0);
     if (heads <= 0) continue;
     const T* src = x + row * x_ld + static_cast<long long>(h0) * D;
@@ -195,7 +245,7 @@ __global__ void __launch_bounds__(kMrThreads) mrope_rows_kernel(const T* x, T* o
 // Blocks 0 .. v_blocks - 1 take the value tiles (64 rows of one head), the
 // others (row, head group) units of the queries and keys.
 template <int D, int N>
-__global__ void __launch_bounds__(kMrThreads) mrope_append_kernel(const MropeAppendArgs a, int v_blocks, int groups) {
+__global__ void __launch_bounds__(kMrThreads, kMrBlocks) mrope_append_kernel(const MropeAppendArgs a, int v_blocks, int groups) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_slots = a.n_pages * 64;
@@ -205,15 +255,17 @@ __global__ void __launch_bounds__(kMrThreads) mrope_append_kernel(const MropeApp
     record_error(a.status, DVLM_ERR_BOUNDS);
     return -1;
   };
-  if (static_cast<int>(blockIdx.x) >= v_blocks) {
+  const bool units = static_cast<int>(blockIdx.x) >= v_blocks;
+  const int idx = static_cast<int>(blockIdx.x) - (units ? v_blocks : 0);
+  if (units) {
     const MrSmem s = mr_carve(smem, a.ax.rot / 2, warp);
     mr_freqs(a.ax, s);
     const Walk first(lane, a.ax.rot / 2 / N);
     const int heads = a.Hq + a.Hkv, hpg = (heads + groups - 1) / groups;
     const long long n_units = static_cast<long long>(a.n_rows) * groups;
     const long long n_warps = static_cast<long long>(gridDim.x - v_blocks) * kMrWarps;
-    for (long long i = static_cast<long long>(blockIdx.x - v_blocks) * kMrWarps + warp; i < n_units; i += n_warps) {
-      const int row = static_cast<int>(i / groups);
+    for (long long i = static_cast<long long>(idx) * kMrWarps + warp; i < n_units; i += n_warps) {
+      const int row = unit_row(i, groups);
       const int h0 = static_cast<int>(i - static_cast<long long>(row) * groups) * hpg, hn = min(hpg, heads - h0);
       const int sl = slot_of(row);
       if (sl < 0 || hn <= 0) continue;
@@ -231,7 +283,7 @@ __global__ void __launch_bounds__(kMrThreads) mrope_append_kernel(const MropeApp
   constexpr int kLd = D + 2;
   bf16* vt = reinterpret_cast<bf16*>(smem);
   int* slot = reinterpret_cast<int*>(vt + kMrVRows * kLd);
-  const int row0 = static_cast<int>(blockIdx.x) / a.Hkv * kMrVRows, g = static_cast<int>(blockIdx.x) % a.Hkv;
+  const int row0 = idx / a.Hkv * kMrVRows, g = idx % a.Hkv;
   const int n = min(kMrVRows, a.n_rows - row0);
   const bf16* src = a.qkv + row0 * a.qkv_ld + (a.Hq + a.Hkv + g) * D;
   if (threadIdx.x < kMrVRows) slot[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? slot_of(row0 + threadIdx.x) : -1;
@@ -288,9 +340,12 @@ int head_groups(int n_rows, int heads) {
   const int want = 148 * 16 / n_rows;
   return want < 1 ? 1 : (want > heads ? heads : want);
 }
-// Blocks for n_units warps of work, at most what the SMs hold at once.
+// Blocks for n_units warps of work, at most twice what the SMs hold at once
+// (a warp then takes two or three rows on one table of frequencies; once the
+// residents: 40 us, unlimited: 41 us, twice: 38.9 us for 16384 rows of 16/2
+// heads of 128).
 int unit_blocks(long long n_units) {
-  const long long b = (n_units + kMrWarps - 1) / kMrWarps, most = static_cast<long long>(device_sm_count()) * 8;
+  const long long b = (n_units + kMrWarps - 1) / kMrWarps, most = static_cast<long long>(device_sm_count()) * 2 * kMrBlocks;
   return static_cast<int>(b < most ? b : most);
 }
 template <typename T, int N>

@@ -14,8 +14,12 @@
 // probabilities, per sequence: the K + 1 rows are never read whole), latency
 // alone.  One cluster per sequence: each of its warps owns a contiguous
 // stretch of the vocabulary and sums it, the CTA totals meet in distributed
-// shared memory, and the one warp whose stretch holds the step walks it again
-// out of L2.  No scratch, no atomics: sums in a fixed order.
+// shared memory, and the CTA whose stretch holds the step divides that
+// stretch among its warps and walks what is left out of L2.  No scratch, no
+// atomics: sums in a fixed order.  The sum takes a widening, a maximum with 0,
+// a conversion and an addition per probability (comparing and selecting each
+// one first took four times the instructions); rows that turn out to hold
+// infinities are summed again with care.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -25,6 +29,7 @@ namespace {
 constexpr int kSvThreads = 512;
 constexpr int kSvWarps = kSvThreads / 32;
 constexpr int kSvMaxCta = 8;
+constexpr int kSvBatch = 4;  // pieces of a row in flight per lane
 
 __device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
@@ -62,27 +67,33 @@ __device__ __forceinline__ double residual(float p, float q) {
   return (p > q && p < INFINITY) ? static_cast<double>(p) - static_cast<double>(q) : 0.0;
 }
 
-// N consecutive probabilities at v (fewer at the row's end: the rest 0).
-template <typename T, bool kVec, int N>
-__device__ __forceinline__ void load_piece(const T* row, int v, int hi, float (&f)[N]) {
-  if constexpr (kVec) {
-    if (v < hi) {  // rows are a whole number of pieces
-      Piece<T>::widen(*reinterpret_cast<const uint4*>(row + v), f);
-      return;
-    }
+// N consecutive probabilities at v as loaded, 0 from hi on (kVec: hi is a
+// whole number of pieces).  No branch: the loads of a batch go out together.
+template <typename T, bool kVec>
+struct Raw {
+  uint4 w;
+  __device__ __forceinline__ void load(const T* row, int v, int hi) {
+    w = make_uint4(0, 0, 0, 0);
+    if (v < hi) w = *reinterpret_cast<const uint4*>(row + v);
   }
-#pragma unroll
-  for (int e = 0; e < N; ++e) f[e] = v + e < hi ? as_f(row[v + e]) : 0.f;
-}
+  __device__ __forceinline__ void widen(float (&f)[Piece<T>::n]) const { Piece<T>::widen(w, f); }
+};
+template <typename T>
+struct Raw<T, false> {
+  float x;
+  __device__ __forceinline__ void load(const T* row, int v, int hi) { x = v < hi ? as_f(row[v]) : 0.f; }
+  __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = x; }
+};
 }  // namespace
 
 // kVec: rows and bases 16-byte aligned, 16-byte pieces; else one element a
 // lane (coalesced all the same).
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kSvThreads) spec_sample_kernel(const SpecSampleArgs a) {
+__global__ void __launch_bounds__(kSvThreads, 2) spec_sample_kernel(const SpecSampleArgs a) {
   constexpr int N = kVec ? Piece<T>::n : 1;
   constexpr int kStep = 32 * N;
   __shared__ double w_tot[kSvWarps];
+  __shared__ double w_sub[kSvWarps];
   __shared__ double c_tot[kSvMaxCta];
   __shared__ int s_k;
   const int n_cta = gridDim.x, rank = blockIdx.x, seq = blockIdx.y;
@@ -135,44 +146,69 @@ __global__ void __launch_bounds__(kSvThreads) spec_sample_kernel(const SpecSampl
   const int steps = (V + kStep - 1) / kStep, per = (steps + n_warp - 1) / n_warp;
   const long long lo_l = static_cast<long long>(rank * kSvWarps + warp) * per * kStep;
   const int lo = static_cast<int>(lo_l < V ? lo_l : V);
-  const int hi = static_cast<int>(lo_l + static_cast<long long>(per) * kStep < V ? lo_l + static_cast<long long>(per) * kStep : V);
+  const int hi = static_cast<int>(min(lo_l + static_cast<long long>(per) * kStep, static_cast<long long>(V)));
 
-  auto values = [&](int v, double (&r)[N]) {
-    float fp[N], fq[N];
-    load_piece<T, kVec, N>(p, v, hi, fp);
+  // Residuals of the piece at v from its probabilities.  careful: NaN and
+  // infinities count as 0; else (no q) an infinity shows in the sum, NaN and
+  // negative values count as 0.
+  auto values = [&](int v, bool careful, const Raw<T, kVec>& wp, const Raw<T, kVec>& wq, double (&r)[N]) {
+    float fp[N];
+    wp.widen(fp);
     if (q) {
-      load_piece<T, kVec, N>(q, v, hi, fq);
-    } else {
+      float fq[N];
+      wq.widen(fq);
 #pragma unroll
-      for (int e = 0; e < N; ++e) fq[e] = v + e == hot ? 1.f : 0.f;
+      for (int e = 0; e < N; ++e) r[e] = residual(fp[e], fq[e]);
+    } else if (careful) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) r[e] = residual(fp[e], v + e == hot ? 1.f : 0.f);
+    } else {
+      if (hot >= v && hot < v + N) {  // (one piece of the row)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (v + e == hot) fp[e] -= 1.f;  // exact where positive: p and 1 within a factor of two
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) r[e] = static_cast<double>(fmaxf(fp[e], 0.f));
+    }
+  };
+  // Sum of the steps from at to end, in every lane; kSvBatch pieces of a row
+  // are on their way at once.
+  auto stretch_sum = [&](int at, int end, bool careful) {
+    double sum = 0.0;
+    for (int v0 = at + lane * N; v0 < end; v0 += kSvBatch * kStep) {
+      Raw<T, kVec> wp[kSvBatch], wq[kSvBatch];
+#pragma unroll
+      for (int i = 0; i < kSvBatch; ++i) wp[i].load(p, v0 + i * kStep, end);
+      if (q) {
+#pragma unroll
+        for (int i = 0; i < kSvBatch; ++i) wq[i].load(q, v0 + i * kStep, end);
+      }
+#pragma unroll
+      for (int i = 0; i < kSvBatch; ++i) {
+        double r[N];
+        values(v0 + i * kStep, careful, wp[i], wq[i], r);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum += r[e];
+      }
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) r[e] = residual(fp[e], fq[e]);
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum;
   };
 
   // u in [0, 1): anything else counts as the nearest value inside, so that a step is always found
   float uf = a.u_sample[seq];
   uf = uf >= 0.f ? fminf(uf, 0x1.fffffep-1f) : 0.f;
   const double u = static_cast<double>(uf);
+  bool careful = false;
   for (int pass = 0;; ++pass) {
-    double sum = 0.0;
-#pragma unroll 4
-    for (int v = lo + lane * N; v < hi; v += kStep) {
-      double r[N];
-      values(v, r);
-#pragma unroll
-      for (int e = 0; e < N; ++e) sum += r[e];
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const double sum = stretch_sum(lo, hi, careful);
     if (lane == 0) w_tot[warp] = sum;
     __syncthreads();
-    double mine = 0.0, before = 0.0;  // this CTA's total, and the warps before this one, in warp order
+    double mine = 0.0;  // this CTA's total, in warp order
 #pragma unroll
-    for (int w = 0; w < kSvWarps; ++w) {
-      if (w == warp) before = mine;
-      mine += w_tot[w];
-    }
+    for (int w = 0; w < kSvWarps; ++w) mine += w_tot[w];
     if (pass == 0) cluster_wait();
     if (threadIdx.x < n_cta) st_dsmem_f64(map_to_cta(smem_u32(&c_tot[rank]), threadIdx.x), mine);
     cluster_sync();
@@ -181,56 +217,93 @@ __global__ void __launch_bounds__(kSvThreads) spec_sample_kernel(const SpecSampl
       if (c == rank) base = total;
       total += c_tot[c];
     }
-    if (total > 0.0) {
+    if (!(total < INFINITY) && !careful) {
+      careful = true;
+    } else if (total > 0.0) {
       const double target = u * total;
-      // this warp's share (base + before, base + before + its sum], as every warp computes it
-      const double from = base + before, to = base + (before + w_tot[warp]);
-      if (from <= target && to > target) {
-        double run = from;
-        int found = -1, last = -1;
-        for (int v0 = lo; v0 < hi && found < 0; v0 += kStep) {
-          double r[N], c[N];
-          const int v = v0 + lane * N;
-          values(v, r);
-          c[0] = r[0];
+      if (base <= target && base + mine > target) {  // the step lies in this CTA's stretches
+        // the warp whose stretch holds it: the first whose end passes the target
+        double from = base, run = 0.0;
+        int ow = 0;
 #pragma unroll
-          for (int e = 1; e < N; ++e) c[e] = c[e - 1] + r[e];
-          double inc = c[N - 1];
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
+        for (int w = 0; w < kSvWarps; ++w) {
+          const bool open = !(base + (run + w_tot[w]) > target);
+          run += w_tot[w];
+          if (open) {
+            ow = w + 1;
+            from = base + run;
+          } else {
+            break;
           }
-          const double ex = inc - c[N - 1];
-          int hit = 0x7fffffff, pos = -1;
-#pragma unroll
-          for (int e = N - 1; e >= 0; --e) {
-            if (r[e] > 0.0 && run + (ex + c[e]) > target) hit = v + e;
-            if (r[e] > 0.0 && pos < 0) pos = v + e;
-          }
-          hit = __reduce_min_sync(0xffffffffu, hit);
-          pos = __reduce_max_sync(0xffffffffu, pos);
-          if (pos >= 0) last = pos;
-          if (hit != 0x7fffffff) found = hit;
-          run += __shfl_sync(0xffffffffu, inc, 31);
         }
-        // rounding in the walk may leave the step just past its end: the last
-        // token of the stretch that has any probability
-        if (lane == 0) a.out_ids[static_cast<size_t>(seq) * (K + 1) + k] = found >= 0 ? found : last;
+        // its steps again, a share per warp
+        const int s_lo = min(V, (rank * kSvWarps + ow) * per * kStep), share = (per + kSvWarps - 1) / kSvWarps;
+        const int s_hi = min(V, s_lo + per * kStep);
+        const int m_lo = min(s_hi, s_lo + warp * share * kStep), m_hi = min(s_hi, m_lo + share * kStep);
+        const double part = stretch_sum(m_lo, m_hi, careful);
+        if (lane == 0) w_sub[warp] = part;
+        __syncthreads();
+        int sw = -1, last_sw = 0;
+        double at = from, sw_from = from;
+#pragma unroll
+        for (int w = 0; w < kSvWarps; ++w) {
+          const double x = w_sub[w];
+          if (x > 0.0) last_sw = w;
+          if (sw < 0 && at + x > target) {
+            sw = w;
+            sw_from = at;
+          }
+          at += x;
+        }
+        // (rounding may leave the step just past the end: then the last token
+        // that has any probability)
+        const bool past = sw < 0;
+        if (warp == (past ? last_sw : sw)) {
+          double walk = sw_from;
+          int found = -1, last = -1;
+          for (int v0 = m_lo; v0 < m_hi && found < 0; v0 += kStep) {
+            double r[N], c[N];
+            const int v = v0 + lane * N;
+            Raw<T, kVec> wp, wq;
+            wp.load(p, v, m_hi);
+            if (q) wq.load(q, v, m_hi);
+            values(v, careful, wp, wq, r);
+            c[0] = r[0];
+#pragma unroll
+            for (int e = 1; e < N; ++e) c[e] = c[e - 1] + r[e];
+            double inc = c[N - 1];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const double o = __shfl_up_sync(0xffffffffu, inc, d);
+              if (lane >= d) inc += o;
+            }
+            const double ex = inc - c[N - 1];
+            int hit = 0x7fffffff, pos = -1;
+#pragma unroll
+            for (int e = N - 1; e >= 0; --e) {
+              if (r[e] > 0.0 && !past && walk + (ex + c[e]) > target) hit = v + e;
+              if (r[e] > 0.0 && pos < 0) pos = v + e;
+            }
+            hit = __reduce_min_sync(0xffffffffu, hit);
+            pos = __reduce_max_sync(0xffffffffu, pos);
+            if (pos >= 0) last = pos;
+            if (hit != 0x7fffffff) found = hit;
+            walk += __shfl_sync(0xffffffffu, inc, 31);
+          }
+          if (lane == 0) a.out_ids[static_cast<size_t>(seq) * (K + 1) + k] = found >= 0 ? found : last;
+        }
       }
       break;
-    }
-    // nothing left of the residual: the target's own row; nothing there
-    // either is an error
-    if (pass == 1) {
+    } else if (q || hot >= 0) {  // nothing left of the residual: the target's own row
+      q = nullptr;
+      hot = -1;
+    } else {  // nothing there either
       if (rank == 0 && threadIdx.x == 0) {
         record_error(a.status, DVLM_ERR_BOUNDS);
         a.out_ids[static_cast<size_t>(seq) * (K + 1) + k] = 0;
       }
       break;
     }
-    q = nullptr;
-    hot = -1;
     cluster_sync();  // c_tot and w_tot have been read
   }
   if (rank == 0) {
@@ -248,11 +321,14 @@ cudaError_t launch_spec_sample(const SpecSampleArgs& a, bool is_bf16, cudaStream
   const bool vec = (static_cast<long long>(a.V) * es) % 16 == 0 &&
                    (reinterpret_cast<uintptr_t>(a.target_p) & 15u) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.draft_p) & 15u) == 0;
-  // CTAs per sequence: the portable cluster size, fewer for vocabularies that
-  // leave its warps without a step
-  const int steps = (a.V + 1023) / 1024;
+  // CTAs per sequence: as many as keep the batch within what the SMs hold at
+  // once (two CTAs each), up to the portable cluster size; fewer for
+  // vocabularies that leave warps without a step of four pieces.  128 rows of
+  // 151936 in bf16: 16.8 us with 2 CTAs each; 28 us with 4 and 40 us with 8
+  // against 22 us with 2 in an earlier form
+  const int steps = (a.V + 1023) / 1024, room = 2 * device_sm_count();
   int n_cta = 1;
-  while (n_cta < kSvMaxCta && n_cta * kSvWarps / 4 < steps) n_cta *= 2;
+  while (n_cta < kSvMaxCta && 2 * n_cta * a.b <= room && n_cta * kSvWarps / 4 < steps) n_cta *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(n_cta, a.b);
   cfg.blockDim = dim3(kSvThreads);
