@@ -11,21 +11,34 @@
 // Tile: the G = Hq / Hkv query heads of a KV head times 128 / G rows fill the
 // 128 lanes of an MMA, so a single-token row of 8 heads costs the cache read
 // once, not 8 times.  A CTA works on two tiles at a time, each with its own
-// softmax warpgroup (a thread owns a row), S and P sharing TMEM columns and O
-// beside them (2 x 128 + 2 x D columns):
+// softmax warpgroup (a thread owns a row):
 //   pair: two neighbouring row tiles of one request and KV head over the same
-//         128-slot chunks (each K and V chunk is loaded once for 256 rows);
-//   solo: one row tile; the two warpgroups take alternate chunks and combine
+//         pages (each K and V page is loaded once for 256 rows);
+//   solo: one row tile; the two warpgroups take alternate pages and combine
 //         their (m, l, O) through TMEM at the end, so that few rows keep both
 //         halves of the SM busy.
-// The tensor pipe alternates between the tiles: while one tile's scores are
-// exponentiated, the other's P V and next Q K^T run.
+// A step is one 64-slot page.  TMEM holds two score buffers of 64 columns per
+// tile (P in bf16 takes the place of its scores) and O of both tiles (2 x 2 x
+// 64 + 2 x D columns): Q K^T of the page after next is issued right behind
+// P V of this one, so that scores wait for the softmax warps and not the other
+// way round.  One thread issues all products, alternating between the tiles.
+//
+// Bound and measure: a page of a pair item takes about 2100 cycles, of which
+// the exponentials of its 256 x 64 scores hold their unit for 1024 and the
+// products the tensor pipe for 1260; chunks of rows run into the 1000 W power
+// cap (1.74 of 1.965 GHz).  4096 rows over 12288 slots, 16/2 heads of 128: 335
+// us, 1.03 PFLOP/s.  Steps of two pages with one score buffer: 340 to 366 us
+// (the scores' latency stands between two steps); four warpgroups with the
+// keys of a page halved between two: 352 us, and with a second issuing thread
+// 350 us at lower clocks; a quarter or half of the exponentials as a
+// polynomial on the multiply-add pipe: 343 and 355 us.  64 single tokens over
+// 900 to 16000 slots read 5.6 TB/s (90 us).
 //
 // Work split: all (request, KV head, pair or solo item) are laid end to end by
 // their cost in slots, and the line is cut into equal parts, one per CTA (one
 // CTA per SM).  A cut inside an item leaves partial (O, m, l) in the workspace
 // (at most two per CTA) for the merge kernel; every other row is written
-// directly.  The cost of a request's items is a closed form (chunk ends grow
+// directly.  The cost of a request's items is a closed form (page ends grow
 // linearly), so each CTA finds its part from the lengths on the device alone:
 // no host knowledge of them, no plan kernel.
 #include <cuda_fp16.h>
@@ -41,7 +54,6 @@ constexpr int kAcKeys = 64;      // slots per step: one page
 constexpr int kAcRing = 4;       // work descriptors in flight
 constexpr int kAcItemCost = 256; // fixed cost of an item, in slot units (prologue and epilogue)
 constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
-constexpr int kAcPrefetch = 8;   // pages brought into L2 ahead of the ring (solo items)
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
 template <int D>
@@ -70,6 +82,7 @@ struct Req {
 __device__ __forceinline__ Req load_req(const ChunkAttnArgs& a, int b, int tpt, int* err) {
   Req r;
   int lo = a.cu_rows[b], hi = a.cu_rows[b + 1], kv = a.kv_len[b];
+  const int noisy = a.n_noisy ? a.n_noisy[b] : 0, hid = a.n_hidden ? a.n_hidden[b] : 0;
   if (lo < 0 || hi < lo || hi > a.n_rows || kv < 0 || kv > a.max_pages * 64LL || hi - lo > kv) {
     *err = 1;  // takes no part
     lo = hi = kv = 0;
@@ -78,8 +91,6 @@ __device__ __forceinline__ Req load_req(const ChunkAttnArgs& a, int b, int tpt, 
   r.n = hi - lo;
   r.kv = kv;
   r.base = kv - r.n;
-  int noisy = a.n_noisy ? a.n_noisy[b] : 0;
-  int hid = a.n_hidden ? a.n_hidden[b] : 0;
   r.nclean = r.n - max(0, min(noisy, r.n));
   r.hid = max(0, min(hid, kv));
   const int tiles = (r.n + tpt - 1) / tpt;
@@ -89,11 +100,11 @@ __device__ __forceinline__ Req load_req(const ChunkAttnArgs& a, int b, int tpt, 
   return r;
 }
 // Cost of the first i pair items of a request: sum of 2 * (visible slots) +
-// kAcItemCost, the slots counted from the hidden prefix's chunk on.
+// kAcItemCost, the slots counted from the hidden prefix's page on.
 __device__ __forceinline__ long long pair_prefix(const Req& r, int tpt, int i) {
   const long long p2 = 2 * tpt, off = r.base - (r.hid & ~(kAcKeys - 1));
   const long long k = min(i, r.pc);
-  long long k0 = off < 0 ? min(k, -off / p2) : 0;  // leading items that end at or before the first visible chunk
+  long long k0 = off < 0 ? min(k, -off / p2) : 0;  // leading items that end at or before the first visible page
   long long c = (k - k0) * off + p2 * (k * (k + 1) / 2 - k0 * (k0 + 1) / 2);
   c += (i - k) * max(0LL, static_cast<long long>(r.kv) - (r.hid & ~(kAcKeys - 1)));
   return 2 * c + static_cast<long long>(i) * kAcItemCost;
@@ -108,14 +119,13 @@ __device__ __forceinline__ long long req_cost(const Req& r, int tpt) {
 // Work descriptor (16 ints in shared memory).
 struct Work {
   int kind;             // 0 end, 1 pair, 2 solo
-  int c0, nc;           // first chunk, chunks
+  int c0, nc;           // first page, pages
   int row0, ntok;       // first row (of all rows) and rows of the item
   int t0;               // the item's first row within the request
   int nclean, base, kv, hid;
   int g;                // KV head
   int slot;             // -1: whole item; 0 / 1: partial, this CTA's slot
-  int b;
-  int pad[3];
+  int pad[4];
 };
 static_assert(sizeof(Work) == 64, "descriptor size");
 
@@ -169,7 +179,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) { return ex2_approx(x); }
 
 // Two fp32 lanes in one 64-bit register (packed multiply-add and add).
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -190,45 +199,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x for two x >= -126 on the multiply-add pipe: x = n + r with n the nearest
-// integer (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^r by the
-// cubic of least relative error on [-1/2, 1/2] (7.5e-5, a Lawson-weighted
-// least-squares fit; P is rounded to bf16, 3.9e-3, right after), n added to the
-// exponent field.
-__device__ __forceinline__ void ex2_poly2(uint64_t x, float& y0, float& y1) {
-  constexpr float kMagic = 12582912.f;
-  const uint64_t t = add2(x, pack2(kMagic, kMagic));
-  const uint64_t n = add2(t, pack2(-kMagic, -kMagic));
-  const uint64_t r = fma2(n, pack2(-1.f, -1.f), x);
-  uint64_t p = fma2(r, pack2(0.05517167f, 0.05517167f), pack2(0.24261113f, 0.24261113f));
-  p = fma2(p, r, pack2(0.69326097f, 0.69326097f));
-  p = fma2(p, r, pack2(0.99992806f, 0.99992806f));
-  float t0, t1, p0, p1;
-  unpack2(t, t0, t1);
-  unpack2(p, p0, p1);
-  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-// p_j = 2^(sl2 s_j + neg) of a 32-column block of scores, packed to bf16;
-// returns their fp32 sum.  kPoly of every 4 pairs go to the polynomial: the
-// exponential unit gives 16 results a clock and SM, which alone would take as
-// long as the products of the tile.  A masked score (-inf) gives 0, or 2^-126
-// from the polynomial: nothing beside any visible slot of the row, and a row
-// without one keeps its maximum at -inf and is set to 0 at the end.
-template <int kPoly>
+// p_j = 2^(sl2 s_j + neg) of a 32-column block of scores, packed to bf16 (P's
+// rounding: half a step of 2^-8 relative, of a weight in a sum whose divisor l
+// is the fp32 sum of the unrounded weights; the tensor pipe takes P and V in
+// one 16-bit type).  Returns the fp32 sum.  A masked score (-inf) gives 0.
 __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], uint64_t sl2, uint64_t neg, uint32_t* pk) {
   uint64_t sum = pack2(0.f, 0.f), sum1 = sum;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), sl2, neg);
-    float x0, x1, p0, p1;
+    float x0, x1;
     unpack2(x, x0, x1);
-    if ((j & 3) < kPoly) {
-      ex2_poly2(pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f)), p0, p1);
-    } else {
-      p0 = ex2(x0);
-      p1 = ex2(x1);
-    }
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
     if (j & 1) sum1 = add2(sum1, pack2(p0, p1));
     else sum = add2(sum, pack2(p0, p1));
     pk[j] = pack_bf16(p0, p1);
@@ -237,8 +219,6 @@ __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], uint64_t sl2
   unpack2(add2(sum, sum1), u, v);
   return u + v;
 }
-constexpr int kAcPoly = 0;
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -289,7 +269,7 @@ __device__ __noinline__ void clear_outside(uint8_t* v, int sw, int hi, int lo) {
 // put right (64-bit integer division costs hundreds of cycles on the one warp
 // that everything waits for).
 __device__ __forceinline__ int div_small(long long a, long long b) {
-  int q = static_cast<int>(static_cast<float>(a) / static_cast<float>(b));
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
   while (q > 0 && q * b > a) --q;
   while ((q + 1) * b <= a) ++q;
   return q;
@@ -406,7 +386,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
     total += s_scan[w];
   }
   const int parts = max(1, min(P, static_cast<int>(min(1.0e6f, static_cast<float>(total) * (1.f / kAcMinPart)))));
-  const long long share = static_cast<long long>(static_cast<float>(total) * 1.000001f / parts) + 1;
+  const long long share =
+      static_cast<long long>(__fdividef(static_cast<float>(total) * 1.00001f, static_cast<float>(parts))) + 1;
   const long long lo = min(total, cta * share), hi = min(total, lo + share);
   long long at = before + inc - mine;
   if (lo < hi && at <= lo && lo < at + mine) {  // one thread's requests hold the first unit
@@ -431,7 +412,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ schedule and load
-    const uint64_t pol = l2_policy_evict_last();
+    // few rows read a cache once, pair items many times
+    const uint64_t pol_once = l2_policy_evict_first(), pol_kept = l2_policy_evict_last();
     int it = 0;        // descriptors issued
     int pos = 0;       // K/V ring position
     int nq = 0;        // Q loads issued
@@ -461,6 +443,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const bool solo = i == r.pairs;
         const long long w = solo ? solo_cost(r) : pair_prefix(r, tpt, i + 1) - pair_prefix(r, tpt, i);
         const long long xa = x - start, xb = min(w, hi - start);
+        const uint64_t pol = solo ? pol_once : pol_kept;
         Work k{};
         k.kind = solo ? 2 : 1;
         k.t0 = i * 2 * tpt;
@@ -472,14 +455,13 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         k.kv = r.kv;
         k.hid = r.hid;
         k.g = g;
-        k.b = b;
         const int te = k.t0 + k.ntok, end = te > r.nclean ? r.kv : r.base + te;
         const int cb = r.hid / kAcKeys, nch = end > r.hid ? (end + kAcKeys - 1) / kAcKeys - cb : 0;
-        // cut positions in chunks; a solo item is cut in pairs of chunks
+        // the part's pages; a solo item is cut between pairs of pages (the CTA
+        // that ends here and the one that goes on compute the same cut)
         const int unit = solo ? 2 : 1;
-        // (the CTA that ends here and the one that goes on compute the same cut)
         const int nu = (nch + unit - 1) / unit;
-        const float scale = static_cast<float>(nu) / static_cast<float>(w);
+        const float scale = __fdividef(static_cast<float>(nu), static_cast<float>(w));
         const int ca = min(nu, static_cast<int>(static_cast<float>(xa) * scale)) * unit;
         const int ce = xb == w ? nch : min(nu, static_cast<int>(static_cast<float>(xb) * scale)) * unit;
         k.c0 = cb + ca;
@@ -516,16 +498,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           const int lag = k.kind == 1 ? 2 : 4;
           const int n_held = (r.kv + 63) >> 6;
           // page numbers: a window of 64 table entries, two per lane, that
-          // moves up by 32 (loads, prefetches and the lagging V stay within 32)
+          // moves up by 32 (V lags K by less than that)
           const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
           int win = k.c0 & ~31;
-          auto entry_at = [&](int p) -> int {
-            if (p >= n_held) return 0;
-            const int v = table[p];
-            if (v >= 0 && v < a.n_pages) return v;
-            record_error(a.status, DVLM_ERR_BOUNDS);
-            return 0;
-          };
+          auto entry_at = [&](int p) { return p < n_held ? table[p] : -1; };
           int w0 = entry_at(win + lane), w1 = entry_at(win + 32 + lane);
           auto page_of = [&](int p) -> int {
             if (p >= win + 64) {
@@ -533,7 +509,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
               w0 = w1;
               w1 = entry_at(win + 32 + lane);
             }
-            return __shfl_sync(0xffffffffu, p < win + 32 ? w0 : w1, p & 31);
+            const int page = __shfl_sync(0xffffffffu, p < win + 32 ? w0 : w1, p & 31);
+            if (page >= 0 && page < a.n_pages) return page;
+            record_error(a.status, DVLM_ERR_BOUNDS);  // (only a page that some row sees)
+            return 0;
           };
           auto load = [&](int c, bool is_v) {
             const int st = pos % NS;
@@ -552,22 +531,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
             }
             ++pos;
           };
-          // The ring holds two chunks.  Where few rows read a long cache (solo)
-          // the chunks behind them are brought into L2 ahead, so that a freed
-          // stage refills at L2's latency: 64 single tokens over 900 to 16000
-          // slots
-          auto prefetch = [&](int c) {
-            const int entry = page_of(k.c0 + c) * a.Hkv + g;
-            if (lane == 0) {
-              for (int d = 0; d < D / 64; ++d) tma_prefetch_2d(&mapK, d * 64, entry * 64);
-              tma_prefetch_2d(&mapV, 0, entry * D);
-            }
-          };
-          int pf = lag;
           for (int c = 0; c < min(lag, k.nc) && ok; ++c) load(c, false);
           for (int c = 0; c < k.nc && ok; ++c) {
-            if (k.kind == 2)
-              for (; pf < k.nc && pf <= c + lag + kAcPrefetch; ++pf) prefetch(pf);
             load(c, true);
             if (ok && c + lag < k.nc) load(c + lag, false);
           }
@@ -580,10 +545,9 @@ __global__ void __launch_bounds__(kAcThreads, 1)
             i = 0;
             if (++g >= a.Hkv) {
               g = 0;
-              do {
-                ++b;
-                r = load_req(a, b, tpt, &bad);
-              } while (r.n == 0);
+              r.n = 0;
+              while (r.n == 0 && ++b < a.n_batch) r = load_req(a, b, tpt, &bad);
+              if (r.n == 0) break;  // (the line ends with the last request: only lengths changed under way come here)
             }
           }
         }
@@ -666,6 +630,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           umma_commit(&kv_empty[pos % NS]);
           ++pos;
         }
+        // Q is free behind the last scores: the next item's loads while this one's last pages run
+        if (ok && nc <= lag) umma_commit(q_empty);
         for (int c = 0; c < nc && ok; ++c) {
           const int vs = pos % NS, ks = (pos + 1) % NS;
           const bool more = c + lag < nc;
@@ -686,12 +652,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
             if (more) issue_s(1, ks);
           }
           if (more) umma_commit(&kv_empty[ks]);
+          if (c + lag + 1 == nc) umma_commit(q_empty);
           pos += more ? 2 : 1;
         }
-        if (ok) {
-          umma_commit(q_empty);
-          mbar_arrive(&d_empty[slot]);
-        }
+        if (ok) mbar_arrive(&d_empty[slot]);
       }
     }
   } else {
@@ -780,7 +744,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           // P then stays below 2^8, and O is seldom rescaled
           const bool move = mx > m + lazy || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? ex2((m - mx) * sl2) : 1.f;
+            const float f = move ? ex2_approx((m - mx) * sl2) : 1.f;
             if (move) m = mx;
             l *= f;
             if (c >= step) {  // once every product of the earlier pages is in O
@@ -802,8 +766,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           const float neg = m == -INFINITY ? 0.f : -m * sl2;
           const uint64_t neg2 = pack2(neg, neg), sl22 = pack2(sl2, sl2);
           uint32_t pk[32];
-          const float sum = exp_block<kAcPoly>(s0, sl22, neg2, pk);
-          l += sum + exp_block<kAcPoly>(s1, sl22, neg2, pk + 16);
+          const float sum = exp_block(s0, sl22, neg2, pk);
+          l += sum + exp_block(s1, sl22, neg2, pk + 16);
           tmem_st32_nowait(tP, pk);
           tmem_wait_st();
         }  // else no row of this warp is one of the item's: its P and O are never used
@@ -813,18 +777,17 @@ __global__ void __launch_bounds__(kAcThreads, 1)
       }
       pos += 2 * k.nc;
       if (!ok) break;
-      if (m == -INFINITY) l = 0.f;  // a row that saw nothing (masked scores may leave 2^-126 each)
       if (k.nc > first && !warp_wait(&o_done[w], no++ & 1)) break;
       tc_fence_after();
       if (solo) {
-        // both warpgroups hold the same rows over alternate chunks: each
+        // both warpgroups hold the same rows over alternate pages: each
         // finishes half of the features from both accumulators
         sML[w * 128 + row] = make_float2(m, l);
         if (!meet()) break;
         const float2 o2 = sML[(w ^ 1) * 128 + row];
         const float mm = fmaxf(m, o2.x);
-        const float a_own = m == -INFINITY ? 0.f : ex2((m - mm) * sl2);
-        const float a_oth = o2.x == -INFINITY ? 0.f : ex2((o2.x - mm) * sl2);
+        const float a_own = m == -INFINITY ? 0.f : ex2_approx((m - mm) * sl2);
+        const float a_oth = o2.x == -INFINITY ? 0.f : ex2_approx((o2.x - mm) * sl2);
         const float a0 = w == 0 ? a_own : a_oth, a1 = w == 0 ? a_oth : a_own;
         const float lt = l * a_own + o2.y * a_oth;
         const bool h0 = k.nc > 0, h1 = k.nc > 1;
@@ -838,7 +801,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           tmem_ld16(tl + kAcColO + col, x);
           tmem_ld16(tl + kAcColO + D + col, y);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)  // an accumulator that no chunk reached holds anything
+          for (int j = 0; j < 16; ++j)  // an accumulator that no page reached holds anything
             x[j] = (h0 && a0 > 0.f ? x[j] * f0 : 0.f) + (h1 && a1 > 0.f ? y[j] * f1 : 0.f);
           store_cols(k, tok, valid, 0, col, x);
         }
@@ -880,58 +843,105 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   }
 }
 
-// Rows of items that were cut: block (p, tile) combines the item that CTA p
-// began and others finished, its partials in CTA order.  A warp takes 32 rows
-// (a lane a row) and D / 8 features.
-constexpr int kAmThreads = 1024;
+// Rows of items that were cut: CTA p's record names the item that it began and
+// others finished; its partials are combined in CTA order.  Every block lists
+// the records for itself, and the warps of the grid share the items' tasks (32
+// rows, a lane a row, by D / 8 features; kAmBatch partials' loads together
+// with their (m, l)), so that one cut item already spreads over the GPU: 16
+// rows over 1360 slots, two items of seven parts, spent 6 us in two blocks and
+// spend 3 us so.
+constexpr int kAmThreads = 512;
+constexpr int kAmBatch = 4;
+constexpr int kAmParts = 8;
 template <int D>
-__global__ void __launch_bounds__(kAmThreads) attn_chunk_merge_kernel(const ChunkAttnArgs a, int P) {
-  griddep_wait();
-  const AcPart ws = ac_carve(a.workspace, P, D);
-  const int p0 = blockIdx.x, tile = blockIdx.y;
-  const int4 r4 = *reinterpret_cast<const int4*>(ws.rec + p0 * 16);  // kind, last CTA, first row, rows
-  const int g = ws.rec[p0 * 16 + 4];
-  if (r4.x == 0 || (r4.x == 2 && tile > 0)) return;
-  const int last = r4.y, row0 = r4.z, ntok = r4.w;
+__global__ void __launch_bounds__(kAmThreads, 1) attn_chunk_merge_kernel(const ChunkAttnArgs a, int P) {
+  __shared__ int4 s_item[kAmThreads];  // first CTA, last CTA, first row, rows
+  __shared__ int2 s_kind[kAmThreads];  // kind, KV head
+  __shared__ int s_base[kAmThreads / 32];
   const int G = a.Hq / a.Hkv, tpt = 128 / G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, part = warp >> 2;
-  const int rt = row / G, rh = row - rt * G, tok = tile * tpt + rt;
-  if (rt >= tpt || tok >= ntok) return;
-  constexpr int F = D / 8;
-  float acc[F];
-#pragma unroll
-  for (int j = 0; j < F; ++j) acc[j] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  auto slot_of = [&](int p) { return (p * 2 + (p == p0 ? 1 : 0)) * 2 + tile; };
-#pragma unroll 4
-  for (int p = p0; p <= last; ++p) m = fmaxf(m, ws.ml[slot_of(p) * 128 + row].x);
-  if (m > -INFINITY) {
-#pragma unroll 4
-    for (int p = p0; p <= last; ++p) {
-      const float2 ml = ws.ml[slot_of(p) * 128 + row];
-      const float* o = ws.o + (static_cast<size_t>(slot_of(p)) * D + part * F) * 128 + row;
-      // a part that saw nothing of the row holds zeros
-      const float e = ml.x == -INFINITY ? 0.f : ex2((ml.x - m) * a.scale_log2);
-      l += e * ml.y;
-#pragma unroll
-      for (int j = 0; j < F; ++j) acc[j] += e * o[j * 128];
-    }
+  const AcPart ws = ac_carve(a.workspace, P, D);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  int4 r4 = make_int4(0, 0, 0, 0);  // kind, last CTA, first row, rows
+  int g0 = 0;
+  if (tid < P) {
+    r4 = *reinterpret_cast<const int4*>(ws.rec + tid * 16);
+    g0 = ws.rec[tid * 16 + 4];
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
-  uint32_t pk[F / 2];
+  const unsigned cut = __ballot_sync(0xffffffffu, r4.x != 0);
+  if (lane == 0) s_base[warp] = __popc(cut);
+  __syncthreads();
+  int at = __popc(cut & ((1u << lane) - 1u)), n_items = 0;
 #pragma unroll
-  for (int j = 0; j < F / 2; ++j) pk[j] = pack_bf16(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-  uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + part * F);
+  for (int w = 0; w < kAmThreads / 32; ++w) {
+    if (w < warp) at += s_base[w];
+    n_items += s_base[w];
+  }
+  if (r4.x != 0) {
+    s_item[at] = make_int4(tid, r4.y, r4.z, r4.w);
+    s_kind[at] = make_int2(r4.x, g0);
+  }
+  __syncthreads();
+  constexpr int F = D / kAmParts;
+  constexpr int kTasks = 2 * 4 * kAmParts;  // tiles, row quarters, feature parts
+  const int n_warps = gridDim.x * (kAmThreads / 32);
+  // (a warp's tasks lie grid-wide apart: the first blocks do not take them all)
+  for (int id = warp * gridDim.x + blockIdx.x; id < n_items * kTasks; id += n_warps) {
+    const int item = id / kTasks, sub = id % kTasks, tile = sub / (4 * kAmParts), part = sub / 4 % kAmParts;
+    const int row = (sub & 3) * 32 + lane;
+    const int4 it = s_item[item];
+    const int kind = s_kind[item].x, g = s_kind[item].y, p0 = it.x, last = it.y, row0 = it.z, ntok = it.w;
+    const int rt = row / G, rh = row - rt * G, tok = tile * tpt + rt;
+    if ((kind == 2 && tile > 0) || rt >= tpt || tok >= ntok) continue;
+    float acc[F];
 #pragma unroll
-  for (int q = 0; q < F / 8; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-  if (a.lse && part == 0) a.lse[at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int j = 0; j < F; ++j) acc[j] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    for (int p = p0; p <= last; p += kAmBatch) {
+      float2 ml[kAmBatch];
+      float o[kAmBatch][F];
+#pragma unroll
+      for (int i = 0; i < kAmBatch; ++i) {
+        const int slot = ((p + i) * 2 + (p + i == p0 ? 1 : 0)) * 2 + tile;
+        ml[i] = p + i <= last ? ws.ml[slot * 128 + row] : make_float2(-INFINITY, 0.f);
+        const float* src = ws.o + (static_cast<size_t>(slot) * D + part * F) * 128 + row;
+#pragma unroll
+        for (int j = 0; j < F; ++j) o[i][j] = p + i <= last ? src[j * 128] : 0.f;
+      }
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kAmBatch; ++i) mn = fmaxf(mn, ml[i].x);
+      const float keep = m == -INFINITY ? 0.f : ex2_approx((m - mn) * a.scale_log2);
+      l *= keep;
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[j] *= keep;
+#pragma unroll
+      for (int i = 0; i < kAmBatch; ++i) {
+        // (a part that saw nothing of the row holds zeros)
+        const float e = ml[i].x == -INFINITY ? 0.f : ex2_approx((ml[i].x - mn) * a.scale_log2);
+        l += e * ml[i].y;
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[j] += e * o[i][j];
+      }
+      m = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t o_at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
+    uint32_t pk[F / 2];
+#pragma unroll
+    for (int j = 0; j < F / 2; ++j) pk[j] = pack_bf16(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    uint2* dst = reinterpret_cast<uint2*>(a.out + o_at * D + part * F);
+#pragma unroll
+    for (int q = 0; q < F / 4; ++q) dst[q] = make_uint2(pk[2 * q], pk[2 * q + 1]);
+    if (a.lse && part == 0) a.lse[o_at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 namespace {
 template <int D>
 cudaError_t run_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkAttnArgs& a, int P,
                       cudaStream_t s) {
+  if (P > kAmThreads) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        AcCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
@@ -939,7 +949,7 @@ cudaError_t run_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensor
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(P, 2);
+  cfg.gridDim = dim3(P);
   cfg.blockDim = dim3(kAmThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
