@@ -128,7 +128,7 @@ def _declare(L: ctypes.CDLL) -> None:
                                        _vp]),
         "dvlm_block_attn_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp]),
         "dvlm_engine_set_trace": (_i, [_vp, _vp, _sz, _vp]),
-        "dvlm_page_plan": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 6),
+        "dvlm_page_plan": (_i, [_vp] * 5 + [_i] * 4 + [_vp] * 7),
         "dvlm_mrope": (_i, [_vp, _vp, _vp, _i, _i, _i, _ll, _ll, _i, _i, _vp, _f, _i, _i, _vp, _vp]),
         "dvlm_mrope_append_paged": (_i, [_vp] * 6 + [_i] * 5 + [_ll, _i, _i, _vp, _f, _i, _vp, _vp]),
         "dvlm_chunk_attn_paged_workspace_size": (_sz, [_i] * 5),
@@ -317,17 +317,17 @@ def _sections(sections):
 
 
 def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batch, max_pages, n_pages, max_rows,
-              kv_len, cu_rows, slot_map, free_count_out, status=None, stream=None) -> None:
+              kv_len, cu_rows, slot_map, free_count_out, held_len=None, status=None, stream=None) -> None:
     """Block tables, row offsets and slot map of a ragged step (dvlm_page_plan)."""
     import torch
     i32, dev = torch.int32, _device("dvlm_page_plan", cache_len)
     _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
           (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
           (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
-          (status, i32, 1))
+          (held_len, i32, n_batch), (status, i32, 1))
     _launch(lib().dvlm_page_plan, "dvlm_page_plan", dev, stream, ptr(cache_len), ptr(new_len), ptr(block_table),
             ptr(free_pages), ptr(free_count), n_batch, max_pages, n_pages, max_rows, ptr(kv_len), ptr(cu_rows),
-            ptr(slot_map), ptr(free_count_out), ptr(status))
+            ptr(slot_map), ptr(free_count_out), ptr(held_len), ptr(status))
 
 
 def _rows(where: str, t, dtype, rows: int, ld: int, width: int, dev: int) -> int:

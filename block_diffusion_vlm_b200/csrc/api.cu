@@ -429,7 +429,7 @@ dvlm_status mrope_axes(MropeAxes* ax, const int32_t* pos, int n_axes, const int*
 dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
                            int32_t* free_pages, const int32_t* free_count, int n_batch, int max_pages, int n_pages,
                            int max_rows, int32_t* kv_len, int32_t* cu_rows, int32_t* slot_map,
-                           int32_t* free_count_out, int* dev_status, dvlm_stream stream) {
+                           int32_t* free_count_out, int32_t* held_len, int* dev_status, dvlm_stream stream) {
   if (!cache_len || !new_len || !block_table || !free_pages || !free_count || !kv_len || !cu_rows || !slot_map ||
       !free_count_out)
     return DVLM_ERR_INVALID_ARG;
@@ -437,8 +437,8 @@ dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int
       n_pages > kMaxPages || max_rows < 1)
     return DVLM_ERR_SHAPE;
   PagePlanArgs a{cache_len, new_len, block_table, free_pages, free_count, n_batch, max_pages, n_pages, max_rows,
-                 kv_len, cu_rows, slot_map, free_count_out, kv_len == cache_len || free_count_out == free_count,
-                 dev_status};
+                 kv_len, cu_rows, slot_map, free_count_out, held_len,
+                 kv_len == cache_len || free_count_out == free_count || held_len, dev_status};
   return cuda_status(launch_page_plan(a, cs(stream)));
 }
 

@@ -344,7 +344,8 @@ struct PagePlanArgs {
   int32_t* cu_rows;           // [n_batch + 1]
   int32_t* slot_map;          // [max_rows]
   int32_t* free_count_out;
-  int in_place;               // kv_len is cache_len or free_count_out is free_count
+  int32_t* held_len;          // [n_batch] slots whose pages a request holds (in/out), or NULL: cache_len
+  int in_place;               // some output is an input array
   int* status;
 };
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t s);

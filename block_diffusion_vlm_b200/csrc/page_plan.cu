@@ -1,8 +1,9 @@
 // Block tables, row offsets, slot map and the free-page stack of one ragged
 // step over a paged cache, from the requests' lengths.
 //
-// Mathematics: with held = ceil(cache / 64) and need = ceil((cache + new) / 64)
-// - held, three prefix sums over the requests (new rows, needed pages, pages
+// Mathematics: with held the pages a request has (ceil(cache / 64), or more
+// where a cache was cut back behind its last step) and need = max(ceil((cache +
+// new) / 64) - held, 0), three prefix sums over the requests (new rows, needed pages, pages
 // given back) place everything: request b's rows start at its row prefix, its
 // i-th new page is number (its page prefix + i) off the top of the stack, and
 // a page given back lands above the old top in request order.  All of it is a
@@ -14,7 +15,7 @@
 // request; what takes time is the chain of lengths, scan, table entry, store.
 // One CTA holds small steps; from kPlanWide rows on the slot map is shared by
 // as many CTAs as have four rows a thread.  Where kv_len or free_count_out is
-// the input array, every CTA's reads have to come before the first write: then
+// the input array, or held_len is updated, every CTA's reads have to come before the first write: then
 // the CTAs are one cluster of eight and meet at its barrier (144000 rows of
 // 512 requests: 20 us, against 7.5 us for a grid of 71).
 #include "kernels.h"
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
   int* s_need = s_row + a.n_batch + 1;      // [n + 1] first new page
   int* s_free = s_need + a.n_batch + 1;     // [n + 1] first page given back
   int* s_cache = s_free + a.n_batch + 1;    // [n] cached lengths
+  int* s_held = s_cache + a.n_batch;        // [n] pages held
   __shared__ long long w_sum[3][kPlanWarps];
   __shared__ int s_rows, s_pages;           // admitted rows and pages
 
@@ -73,29 +75,32 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
 
   // each thread takes kPlanPer consecutive requests (as few as n needs)
   const int per = (n + kPlanThreads - 1) / kPlanThreads;
-  int want[kPlanPer], need[kPlanPer], freed[kPlanPer], cache[kPlanPer];
-  bool live[kPlanPer];
+  int want[kPlanPer], need[kPlanPer], freed[kPlanPer], cache[kPlanPer], held[kPlanPer];
+  bool live[kPlanPer], part[kPlanPer];
   long long t0 = 0, t1 = 0, t2 = 0;
 #pragma unroll
   for (int i = 0; i < kPlanPer; ++i) {
     const int b = tid * per + i;
-    want[i] = need[i] = freed[i] = cache[i] = 0;
+    want[i] = need[i] = freed[i] = cache[i] = held[i] = 0;
     live[i] = true;
+    part[i] = false;
     if (i >= per || b >= n) continue;
-    const int c = a.cache_len[b], m = a.new_len[b];
-    if (c < 0 || c > cap || m < -1) {
+    const int c = a.cache_len[b], m = a.new_len[b], hl = a.held_len ? max(a.held_len[b], c) : c;
+    if (c < 0 || hl > cap || m < -1) {
       err = DVLM_ERR_BOUNDS;  // such a request takes no part
       continue;
     }
+    part[i] = true;
     cache[i] = c;
+    held[i] = (hl + 63) >> 6;
     if (m < 0) {
       live[i] = false;
-      freed[i] = (c + 63) >> 6;
+      freed[i] = held[i];
     } else if (c + static_cast<long long>(m) > cap) {
       err = DVLM_ERR_BOUNDS;
     } else {
       want[i] = m;
-      need[i] = ((c + m + 63) >> 6) - ((c + 63) >> 6);
+      need[i] = max(((c + m + 63) >> 6) - held[i], 0);
     }
     t0 += want[i];
     t1 += need[i];
@@ -130,6 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
     fits[i] = false;
     if (i >= per || b >= n) continue;
     s_cache[b] = cache[i];
+    s_held[b] = held[i];
     s_row[b] = static_cast<int>(r0 < a.max_rows ? r0 : a.max_rows);
     s_need[b] = static_cast<int>(r1 < avail ? r1 : avail);
     s_free[b] = static_cast<int>(r2);
@@ -172,6 +178,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
       if (i >= per || b >= n) continue;
       a.kv_len[b] = live[i] ? cache[i] + (fits[i] ? want[i] : 0) : 0;
       a.cu_rows[b] = s_row[b];
+      if (a.held_len && part[i]) a.held_len[b] = live[i] ? max(a.held_len[b], cache[i] + (fits[i] ? want[i] : 0)) : 0;
     }
     if (tid == 0) {
       a.cu_rows[n] = rows;
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
   const int gtid = rank * kPlanThreads + tid, gsize = n_cta * kPlanThreads;
   for (int i = gtid; i < pages; i += gsize) {
     const int b = owner_of(s_need, n, i);
-    a.block_table[static_cast<size_t>(b) * a.max_pages + ((s_cache[b] + 63) >> 6) + (i - s_need[b])] = taken(i);
+    a.block_table[static_cast<size_t>(b) * a.max_pages + s_held[b] + (i - s_need[b])] = taken(i);
   }
   for (long long r = gtid; r < total_freed - pages; r += gsize) {
     if (count + r < a.n_pages) a.free_pages[count + r] = returned(static_cast<int>(r));
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
           ++b;
           last = -1;
         }
-        const int slot = s_cache[b] + (i + e - s_row[b]), p = slot >> 6, held = (s_cache[b] + 63) >> 6;
+        const int slot = s_cache[b] + (i + e - s_row[b]), p = slot >> 6, held = s_held[b];
         if (p != last) {
           page = p < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + p] : taken(s_need[b] + p - held);
           last = p;
@@ -231,10 +238,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
 }
 
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t s) {
-  const int smem = (4 * a.n_batch + 3) * 4;
+  const int smem = (5 * a.n_batch + 3) * 4;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kPlanMaxBatch + 3) * 4);
+                                         (5 * kPlanMaxBatch + 3) * 4);
     if (e != cudaSuccess) return e;
   }
   const bool in_place = a.in_place != 0;

@@ -294,9 +294,13 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * wanted any).  Outputs: kv_len [n_batch] (slots after the step; 0 for a
  * finished request), cu_rows [n_batch + 1], slot_map [max_rows] (page * 64 +
  * row in page of every row; -1 behind the last request's rows),
- * free_count_out [1].  kv_len may be cache_len and free_count_out may be
- * free_count; no other arrays may overlap.  A request whose cached length is
- * outside 0 .. 64 max_pages, whose new length is below -1, or whose sum is
+ * free_count_out [1].  held_len [n_batch] (in/out, may be NULL): slots whose
+ * pages a request still holds where its cache was cut back behind its last
+ * step (dvlm_spec_verify_sample); the plan then counts ceil(max(held_len,
+ * cache_len) / 64) pages as held, and sets it to the larger of itself and
+ * kv_len (0 for a finished request).  kv_len may be cache_len and
+ * free_count_out may be free_count; no other arrays may overlap.  A request whose cached or held
+ * length is outside 0 .. 64 max_pages, whose new length is below -1, or whose sum is
  * past 64 max_pages takes no part (kv_len: 0 in the first two cases, its
  * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
@@ -306,8 +310,8 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
 DVLM_API dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
                                    int32_t* free_pages, const int32_t* free_count, int n_batch, int max_pages,
                                    int n_pages, int max_rows, int32_t* kv_len, int32_t* cu_rows,
-                                   int32_t* slot_map, int32_t* free_count_out, int* dev_status,
-                                   dvlm_stream stream);
+                                   int32_t* slot_map, int32_t* free_count_out, int32_t* held_len,
+                                   int* dev_status, dvlm_stream stream);
 
 /* Rotary positions with several axes (rows of images and video have a time, a
  * height and a width position; text rows the same value on every axis).  The

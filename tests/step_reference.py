@@ -7,33 +7,40 @@ import numpy as np
 PAGE = 64
 
 
-def page_plan(cache_len, new_len, table, stack, max_pages, n_pages, max_rows):
-    """stack: the free pages, top last.  Returns kv_len, cu_rows, slot_map, table, stack, waited, bad."""
+def page_plan(cache_len, new_len, table, stack, max_pages, n_pages, max_rows, held_len=None):
+    """stack: the free pages, top last.  Returns kv_len, cu_rows, slot_map, table, stack, waited, bad, held_len."""
     table, stack, cap = np.array(table), list(stack), max_pages * PAGE
     bad = waited = False
+    hold = [max(h, c) for h, c in zip(cache_len if held_len is None else held_len, cache_len)]
+    held_out = [int(h) for h in (held_len if held_len is not None else cache_len)]
     for b, (c, m) in enumerate(zip(cache_len, new_len)):
-        if m == -1 and 0 <= c <= cap:
-            stack += [int(p) for p in table[b, :-(-c // PAGE)]]
+        if m == -1 and 0 <= c and hold[b] <= cap:
+            stack += [int(p) for p in table[b, :-(-hold[b] // PAGE)]]
+            held_out[b] = 0
     kv, cu, slots, blocked = [], [0], [], False
     for b, (c, m) in enumerate(zip(cache_len, new_len)):
-        if c < 0 or c > cap or m < -1:
+        if c < 0 or hold[b] > cap or m < -1:
             bad, c, m = True, 0, 0
         elif m == -1:
             c, m = 0, 0
-        elif c + m > cap:
-            bad, m = True, 0
         else:
-            have, want = -(-c // PAGE), -(-(c + m) // PAGE)
-            if blocked or want - have > len(stack) or cu[-1] + m > max_rows:
-                waited |= m > 0
-                blocked, m = True, 0
+            if c + m > cap:
+                bad, m = True, 0
             else:
-                for i in range(have, want):
-                    table[b, i] = stack.pop()
-                slots += [int(table[b, (c + t) // PAGE]) * PAGE + (c + t) % PAGE for t in range(m)]
+                have = -(-hold[b] // PAGE)
+                want = max(-(-(c + m) // PAGE), have)
+                if blocked or want - have > len(stack) or cu[-1] + m > max_rows:
+                    waited |= m > 0
+                    blocked, m = True, 0
+                else:
+                    for i in range(have, want):
+                        table[b, i] = stack.pop()
+                    slots += [int(table[b, (c + t) // PAGE]) * PAGE + (c + t) % PAGE for t in range(m)]
+            held_out[b] = max(held_out[b], c + m)
         kv.append(c + m)
         cu.append(cu[-1] + m)
-    return kv, cu, slots + [-1] * (max_rows - len(slots)), table, stack[:n_pages], waited, bad or len(stack) > n_pages
+    return (kv, cu, slots + [-1] * (max_rows - len(slots)), table, stack[:n_pages], waited, bad or len(stack) > n_pages,
+            held_out)
 
 
 def mrope_axis(sections, interleaved, j):

@@ -170,7 +170,7 @@ def _plan(**kw):
     a = dict(cache=16, new=16, table=16, free=16, count=16, n=4, mp=8, np=32, rows=64, kv=16, cu=16, slots=16, out=16)
     a.update(kw)
     return dv.lib().dvlm_page_plan(a["cache"], a["new"], a["table"], a["free"], a["count"], a["n"], a["mp"], a["np"],
-                                   a["rows"], a["kv"], a["cu"], a["slots"], a["out"], None, None)
+                                   a["rows"], a["kv"], a["cu"], a["slots"], a["out"], None, None, None)
 
 
 def test_page_plan_host_validation(dvlm_lib):

@@ -26,7 +26,7 @@ def i32(a, dev):
 
 
 # ------------------------------------------------------------------ page plan
-def run_plan(cuda, cache, new, table, stack, n_pages, max_rows, in_place=False, offset=0, stream=None):
+def run_plan(cuda, cache, new, table, stack, n_pages, max_rows, in_place=False, offset=0, stream=None, held=None):
     n, max_pages = table.shape
     free = np.full(n_pages, -7, dtype=np.int32)
     free[:len(stack)] = stack
@@ -36,17 +36,20 @@ def run_plan(cuda, cache, new, table, stack, n_pages, max_rows, in_place=False, 
     co = d["count"] if in_place else i32([-9], cuda)
     cu = i32([-9] * (n + 1), cuda)
     slots = torch.full((max_rows + offset,), -9, dtype=torch.int32, device=cuda)[offset:]
-    st = status(cuda)
+    st, hd = status(cuda), i32(held, cuda) if held is not None else None
     dv.page_plan(d["cache"], d["new"], d["table"], d["free"], d["count"], n_batch=n, max_pages=max_pages,
                  n_pages=n_pages, max_rows=max_rows, kv_len=kv, cu_rows=cu, slot_map=slots, free_count_out=co,
-                 status=st, stream=stream)
+                 held_len=hd, status=st, stream=stream)
     torch.cuda.synchronize()
-    return [t.cpu().numpy() for t in (kv, cu, slots, d["table"], d["free"], co)] + [int(st.item())]
+    got = [t.cpu().numpy() for t in (kv, cu, slots, d["table"], d["free"], co)] + [int(st.item())]
+    return got + [hd.cpu().numpy() if hd is not None else None]
 
 
-def check_plan(cuda, cache, new, table, stack, n_pages, max_rows, **kw):
-    want = ref.page_plan(cache, new, table, stack, table.shape[1], n_pages, max_rows)
-    kv, cu, slots, tab, free, count, st = run_plan(cuda, cache, new, table, stack, n_pages, max_rows, **kw)
+def check_plan(cuda, cache, new, table, stack, n_pages, max_rows, held=None, **kw):
+    want = ref.page_plan(cache, new, table, stack, table.shape[1], n_pages, max_rows, held)
+    kv, cu, slots, tab, free, count, st, hd = run_plan(cuda, cache, new, table, stack, n_pages, max_rows, held=held, **kw)
+    if held is not None:
+        np.testing.assert_array_equal(hd, want[7])
     np.testing.assert_array_equal(kv, want[0])
     np.testing.assert_array_equal(cu, want[1])
     np.testing.assert_array_equal(slots, want[2])
@@ -84,6 +87,29 @@ def test_page_plan(cuda, n, max_pages, max_new, spare, rows, in_place):
     for seed in range(3):
         cache, new, table, stack, n_pages = plan_case(np.random.default_rng(seed), n, max_pages, max_new, spare)
         check_plan(cuda, cache, new, table, stack, n_pages, rows, in_place=in_place)
+
+
+@pytest.mark.parametrize("n,rows", [(1, 64), (40, 3000), (300, 9000)])
+def test_page_plan_after_a_cut(cuda, n, rows):
+    """Caches cut back behind their last step keep their pages: none is taken twice, all go back at the end."""
+    rng = np.random.default_rng(n)
+    held, new, table, stack, n_pages = plan_case(rng, n, 6, 40, 60)
+    cache = np.maximum(held - rng.integers(0, 90, n), 0)
+    for h in (held, np.where(rng.random(n) < 0.3, -5, held)):      # a held length below the cached one counts as that
+        check_plan(cuda, np.where(h < 0, held, cache), new, table, stack, n_pages, rows, held=h)
+    bad = held.copy()
+    bad[0] = 6 * 64 + 1
+    check_plan(cuda, cache, new, table, stack, n_pages, rows, held=bad)
+    # a run of steps: what the requests hold and the stack together stay the whole store
+    stack = list(stack)
+    for step in range(6):
+        new = np.array([rng.choice([0, 1, 16, 30]) for _ in range(n)])
+        new = np.where(cache + new > 6 * 64, 0, new)
+        kv, cu, slots, table, free, count, st, held = run_plan(cuda, cache, new, table, stack, n_pages, rows, held=held)
+        stack = free[:int(count[0])].tolist()
+        owned = [int(p) for b in range(n) for p in table[b, :-(-int(held[b]) // 64)]]
+        assert sorted(owned + stack) == list(range(n_pages))
+        cache = np.maximum(kv - rng.integers(0, 14, n), 0)
 
 
 def test_page_plan_waits_in_order(cuda):
