@@ -269,14 +269,19 @@ def selftest_wait_timeout(budget_cycles: int, status, gave_up, stream=None) -> N
 
 
 # ---------------------------------------------------------------- batched step over paged caches
-def _take(where: str, dev: int, *args) -> None:
-    """Refuse tensors the library would misread: args are (tensor, dtype, least
-    number of elements) triples; all contiguous, all on GPU number dev."""
+def _take(where: str, dev: int, *args) -> list:
+    """Device addresses of tensors, refusing those the library would misread: args are (tensor, dtype,
+    least number of elements) triples; all contiguous, all on GPU number dev.  None stays None."""
+    out = []
     for t, dtype, least in args:
-        if t is not None and (t.dtype is not dtype or t.numel() < least or t.get_device() != dev
-                              or not t.is_contiguous()):
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.numel() >= least and t.get_device() == dev and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
             raise DvlmError(1, f"{where}: expected a contiguous {dtype} tensor of at least {least} elements on "
                                f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return out
 
 
 def _device(where: str, t) -> int:
@@ -287,12 +292,20 @@ def _device(where: str, t) -> int:
     return dev
 
 
+def _raw_stream(dev: int) -> int:
+    """Handle of torch's current stream on a GPU (the direct query where this torch has it: the
+    stream object costs a microsecond, a sixth of a small call)."""
+    import torch
+    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return query(dev) if query is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _launch(fn, where: str, dev: int, stream, *args) -> None:
     """Call an entry point whose last argument is the stream, with GPU dev
     current (a NULL stream is torch's current one on that GPU)."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if dev == torch.cuda.current_device():
@@ -321,13 +334,11 @@ def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batc
     """Block tables, row offsets and slot map of a ragged step (dvlm_page_plan)."""
     import torch
     i32, dev = torch.int32, _device("dvlm_page_plan", cache_len)
-    _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
-          (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
-          (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
-          (held_len, i32, n_batch), (status, i32, 1))
-    _launch(lib().dvlm_page_plan, "dvlm_page_plan", dev, stream, ptr(cache_len), ptr(new_len), ptr(block_table),
-            ptr(free_pages), ptr(free_count), n_batch, max_pages, n_pages, max_rows, ptr(kv_len), ptr(cu_rows),
-            ptr(slot_map), ptr(free_count_out), ptr(held_len), ptr(status))
+    p = _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
+              (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
+              (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
+              (held_len, i32, n_batch), (status, i32, 1))
+    _launch(lib().dvlm_page_plan, "dvlm_page_plan", dev, stream, *p[:5], n_batch, max_pages, n_pages, max_rows, *p[5:])
 
 
 def _rows(where: str, t, dtype, rows: int, ld: int, width: int, dev: int) -> int:
@@ -357,9 +368,9 @@ def mrope(x, out, pos, *, n_rows, n_heads, D, sections, rope_base, dtype, rot_di
     x_ld = _rows("dvlm_mrope", x, td, n_rows, x_ld, n_heads * D, dev)
     out_ld = _rows("dvlm_mrope", out, td, n_rows, out_ld, n_heads * D, dev)
     sec = _sections(sections)
-    _take("dvlm_mrope", dev, (pos, torch.int32, len(sec) * n_rows), (status, torch.int32, 1))
-    _launch(lib().dvlm_mrope, "dvlm_mrope", dev, stream, ptr(x), ptr(out), ptr(pos), n_rows, n_heads, D, x_ld, out_ld,
-            rot_dim or D, len(sec), sec, float(rope_base), int(interleaved), dtype, ptr(status))
+    p = _take("dvlm_mrope", dev, (pos, torch.int32, len(sec) * n_rows), (status, torch.int32, 1))
+    _launch(lib().dvlm_mrope, "dvlm_mrope", dev, stream, x.data_ptr(), out.data_ptr(), p[0], n_rows, n_heads, D, x_ld,
+            out_ld, rot_dim or D, len(sec), sec, rope_base, interleaved, dtype, p[1])
 
 
 def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, Hq, Hkv, D, n_pages, sections,
@@ -369,12 +380,11 @@ def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, H
     dev, bf = _device("dvlm_mrope_append_paged", qkv), torch.bfloat16
     qkv_ld = _rows("dvlm_mrope_append_paged", qkv, bf, n_rows, qkv_ld, (Hq + 2 * Hkv) * D, dev)
     sec = _sections(sections)
-    _take("dvlm_mrope_append_paged", dev, (pos, torch.int32, len(sec) * n_rows), (slot_map, torch.int32, n_rows),
-          (q_out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D), (v_pages, bf, n_pages * Hkv * 64 * D),
-          (status, torch.int32, 1))
-    _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, ptr(qkv), ptr(pos), ptr(slot_map),
-            ptr(q_out), ptr(k_pages), ptr(v_pages), n_rows, Hq, Hkv, D, n_pages, qkv_ld, rot_dim or D, len(sec), sec,
-            float(rope_base), int(interleaved), ptr(status))
+    p = _take("dvlm_mrope_append_paged", dev, (pos, torch.int32, len(sec) * n_rows), (slot_map, torch.int32, n_rows),
+              (q_out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
+              (v_pages, bf, n_pages * Hkv * 64 * D), (status, torch.int32, 1))
+    _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, qkv.data_ptr(), *p[:5], n_rows, Hq,
+            Hkv, D, n_pages, qkv_ld, rot_dim or D, len(sec), sec, rope_base, interleaved, p[5])
 
 
 def chunk_attn_paged_workspace_size(n_batch: int, n_rows: int, Hq: int, Hkv: int, D: int) -> int:
@@ -388,16 +398,12 @@ def chunk_attn_paged(q, out, k_pages, v_pages, block_table, kv_len, cu_rows, *, 
     import torch
     dev, bf, i32 = _device("dvlm_chunk_attn_paged", q), torch.bfloat16, torch.int32
     q_ld = _rows("dvlm_chunk_attn_paged", q, bf, n_rows, q_ld, Hq * D, dev)
-    _take("dvlm_chunk_attn_paged", dev, (out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
-          (v_pages, bf, n_pages * Hkv * 64 * D), (block_table, i32, n_batch * max_pages), (kv_len, i32, n_batch),
-          (cu_rows, i32, n_batch + 1), (n_noisy, i32, n_batch), (n_hidden, i32, n_batch),
-          (lse, torch.float32, n_rows * Hq), (status, i32, 1))
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise DvlmError(1, f"dvlm_chunk_attn_paged: the workspace is not a contiguous tensor on cuda:{dev}")
-    _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, ptr(q), ptr(out), ptr(k_pages),
-            ptr(v_pages), ptr(block_table), ptr(kv_len), ptr(cu_rows), ptr(n_noisy), ptr(n_hidden), ptr(lse), n_batch,
-            n_rows, n_pages, max_pages, Hq, Hkv, D, q_ld, float(scale), ptr(workspace),
-            workspace.numel() * workspace.element_size(), ptr(status))
+    p = _take("dvlm_chunk_attn_paged", dev, (out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
+              (v_pages, bf, n_pages * Hkv * 64 * D), (block_table, i32, n_batch * max_pages), (kv_len, i32, n_batch),
+              (cu_rows, i32, n_batch + 1), (n_noisy, i32, n_batch), (n_hidden, i32, n_batch),
+              (lse, torch.float32, n_rows * Hq), (workspace, workspace.dtype, 0), (status, i32, 1))
+    _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, q.data_ptr(), *p[:9], n_batch, n_rows,
+            n_pages, max_pages, Hq, Hkv, D, q_ld, scale, p[9], workspace.numel() * workspace.element_size(), p[10])
 
 
 def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K, V, dtype, accept_len, out_ids,
@@ -406,13 +412,11 @@ def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K
     import torch
     dev, i32, f32 = _device("dvlm_spec_verify_sample", target_p), torch.int32, torch.float32
     td = f32 if dtype == DVLM_FP32 else torch.bfloat16
-    _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
-          (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),
-          (accept_len, i32, b), (out_ids, i32, b * (K + 1)), (cache_len, i32, b), (cache_len_out, i32, b),
-          (status, i32, 1))
-    _launch(lib().dvlm_spec_verify_sample, "dvlm_spec_verify_sample", dev, stream, ptr(target_p), ptr(draft_p),
-            ptr(draft_ids), ptr(n_draft), ptr(u_accept), ptr(u_sample), b, K, V, dtype, ptr(accept_len), ptr(out_ids),
-            ptr(cache_len), ptr(cache_len_out), ptr(status))
+    p = _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
+              (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),
+              (accept_len, i32, b), (out_ids, i32, b * (K + 1)), (cache_len, i32, b), (cache_len_out, i32, b),
+              (status, i32, 1))
+    _launch(lib().dvlm_spec_verify_sample, "dvlm_spec_verify_sample", dev, stream, *p[:6], b, K, V, dtype, *p[6:])
 
 
 # ---------------------------------------------------------------- engine

@@ -247,6 +247,10 @@ cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t s) {
   const bool in_place = a.in_place != 0;
   const int per = kPlanThreads * 4, wide = (a.max_rows + per - 1) / per;
   const int n_cta = a.max_rows < kPlanWide ? 1 : in_place ? kPlanCtas : (wide < device_sm_count() ? wide : device_sm_count());
+  if (!in_place) {  // (a plain launch costs the host half of one with attributes)
+    page_plan_kernel<<<n_cta, kPlanThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(n_cta);
   cfg.blockDim = dim3(kPlanThreads);
@@ -254,7 +258,7 @@ cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = in_place ? n_cta : 1;
+  at[0].val.clusterDim.x = n_cta;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
