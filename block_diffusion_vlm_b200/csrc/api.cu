@@ -7,6 +7,7 @@
 #include <new>
 
 #include "engine.h"
+#include "step.h"
 
 using namespace dvlm;
 

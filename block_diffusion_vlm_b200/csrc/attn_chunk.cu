@@ -41,10 +41,8 @@
 // directly.  The cost of a request's items is a closed form (page ends grow
 // linearly), so each CTA finds its part from the lengths on the device alone:
 // no host knowledge of them, no plan kernel.
-#include <cuda_fp16.h>
-
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step.h"
 
 namespace dvlm {
 

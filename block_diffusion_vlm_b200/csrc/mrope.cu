@@ -19,8 +19,8 @@
 // feature-major in its page: separate blocks turn 64-row tiles of a value
 // head through shared memory; eight rows on eight aligned slots of a page
 // leave as 16-byte pieces.
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step.h"
 
 namespace dvlm {
 

@@ -18,8 +18,8 @@
 // the input array, or held_len is updated, every CTA's reads have to come before the first write: then
 // the CTAs are one cluster of eight and meet at its barrier (144000 rows of
 // 512 requests: 20 us, against 7.5 us for a grid of 71).
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step.h"
 
 namespace dvlm {
 

@@ -20,8 +20,8 @@
 // a conversion and an addition per probability (comparing and selecting each
 // one first took four times the instructions); rows that turn out to hold
 // infinities are summed again with care.
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step.h"
 
 namespace dvlm {
 
