@@ -100,10 +100,10 @@ __device__ __forceinline__ Req load_req(const ChunkAttnArgs& a, int b, int tpt, 
 // Cost of the first i pair items of a request: sum of 2 * (visible slots) +
 // kAcItemCost, the slots counted from the hidden prefix's page on.
 __device__ __forceinline__ long long pair_prefix(const Req& r, int tpt, int i) {
-  const long long p2 = 2 * tpt, off = r.base - (r.hid & ~(kAcKeys - 1));
+  const int p2 = 2 * tpt, off = r.base - (r.hid & ~(kAcKeys - 1));
   const long long k = min(i, r.pc);
-  long long k0 = off < 0 ? min(k, -off / p2) : 0;  // leading items that end at or before the first visible page
-  long long c = (k - k0) * off + p2 * (k * (k + 1) / 2 - k0 * (k0 + 1) / 2);
+  const long long k0 = off < 0 ? min(min(i, r.pc), -off / p2) : 0;  // leading items that end at or before the first visible page
+  long long c = (k - k0) * off + p2 * ((k * (k + 1) - k0 * (k0 + 1)) / 2);
   c += (i - k) * max(0LL, static_cast<long long>(r.kv) - (r.hid & ~(kAcKeys - 1)));
   return 2 * c + static_cast<long long>(i) * kAcItemCost;
 }
@@ -274,11 +274,11 @@ __device__ __forceinline__ int div_small(long long a, long long b) {
 }
 }  // namespace
 
-// Partial results in the workspace: per CTA two slots of two tiles, O [D][128]
-// fp32 (feature-major: a warp stores 32 rows of a feature at once) and (m, l)
+// Partial results in the workspace: per CTA two slots of two tiles, O [D / 4]
+// [128][4] fp32 (a warp stores four features of 32 rows as 512 bytes) and (m, l)
 // [128]; then one merge record per CTA.
 struct AcPart {
-  float* o;       // [P][2][2][D][128]
+  float* o;       // [P][2][2][D / 4][128][4]
   float2* ml;     // [P][2][2][128]
   int* rec;       // [P][16]
 };
@@ -333,16 +333,18 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   const int G = a.Hq / a.Hkv, tpt = 128 / G;
   const AcPart ws = ac_carve(a.workspace, P, D);
 
-  if (tid == 0) {
-    for (int i = 0; i < C::kBars; ++i) {
+  if (warp == kAcThreads / 32 - 1) {  // (a warp that has no length to wait for in small batches)
+    for (int i = lane; i < C::kBars; i += 32) {
       uint64_t* b = &bars[i];
       mbar_init(b, (b >= d_empty && b < q_full) ? 9 : (b >= p_full && b < pv_done) ? 4 : b == x_bar ? 8 : 1);
     }
-    *sabort = 0;
     fence_mbar_init();
-    tma_prefetch_map(&mapQ);
-    tma_prefetch_map(&mapK);
-    tma_prefetch_map(&mapV);
+    if (lane == 0) {
+      *sabort = 0;
+      tma_prefetch_map(&mapQ);
+      tma_prefetch_map(&mapK);
+      tma_prefetch_map(&mapV);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -684,9 +686,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         dst[1] = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]), pack_bf16(x[12], x[13]),
                             pack_bf16(x[14], x[15]));
       } else {
-        float* dst = ws.o + ((static_cast<size_t>(cta * 2 + k.slot) * 2 + tile) * D + col) * 128 + row;
+        float* dst = ws.o + ((static_cast<size_t>(cta * 2 + k.slot) * 2 + tile) * D + col) * 128 + row * 4;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) dst[j * 128] = x[j];
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(dst + j * 128) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
       }
     };
     if (tid == 64) griddep_launch_dependents();
@@ -902,9 +905,16 @@ __global__ void __launch_bounds__(kAmThreads, 1) attn_chunk_merge_kernel(const C
       for (int i = 0; i < kAmBatch; ++i) {
         const int slot = ((p + i) * 2 + (p + i == p0 ? 1 : 0)) * 2 + tile;
         ml[i] = p + i <= last ? ws.ml[slot * 128 + row] : make_float2(-INFINITY, 0.f);
-        const float* src = ws.o + (static_cast<size_t>(slot) * D + part * F) * 128 + row;
+        const float* src = ws.o + (static_cast<size_t>(slot) * D + part * F) * 128 + row * 4;
 #pragma unroll
-        for (int j = 0; j < F; ++j) o[i][j] = p + i <= last ? src[j * 128] : 0.f;
+        for (int j = 0; j < F; j += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p + i <= last) v = *reinterpret_cast<const float4*>(src + j * 128);
+          o[i][j] = v.x;
+          o[i][j + 1] = v.y;
+          o[i][j + 2] = v.z;
+          o[i][j + 3] = v.w;
+        }
       }
       float mn = m;
 #pragma unroll
