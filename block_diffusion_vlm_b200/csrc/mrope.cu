@@ -17,17 +17,25 @@
 // an SM are in different phases and the loads never pause (a block building a
 // table for 32 rows first reached half the bandwidth).  V is stored
 // feature-major in its page: separate blocks turn 64-row tiles of a value
-// head through shared memory; eight rows on eight aligned slots of a page
-// leave as 16-byte pieces.
+// head through shared memory, all of a thread's loads out at once; eight rows
+// on eight aligned slots of a page leave as 16-byte pieces.
+//
+// Measured: 16384 rows of 16/2 heads of 128, 35.9 us (168 MB: 4.7 TB/s; a plain
+// copy of 80 MB to another 80 MB takes 27 us); 1357 rows of 14/2 heads of 64,
+// 5.4 us; one block of 16 rows, 3.1 us; 4999 rows of 16 heads of 80 in fp32,
+// 11.8 us.  Blocks of 256 threads: 38.0, 4.7, 3.5 and 12.0 us.  Value
+// tiles of 32 rows: 39.8 and 4.8 us for the first two.  Values turned by the
+// block that turns their rows, instead of by blocks of their own: 50 us.  Rows
+// brought in by bulk copies, a ring of rows per warp: 37 us.
 #include "ptx.cuh"
 #include "step.h"
 
 namespace dvlm {
 
 namespace {
-constexpr int kMrThreads = 256;
+constexpr int kMrThreads = 128;
 constexpr int kMrWarps = kMrThreads / 32;
-constexpr int kMrBlocks = 4;                // resident blocks per SM (64 registers a thread)
+constexpr int kMrBlocks = 8;                // resident blocks per SM (64 registers a thread)
 constexpr int kMrBatch = 3;                 // pieces in flight per lane
 constexpr int kMrVRows = 64;                // rows of a value tile
 constexpr double kInv2Pi = 0.15915494309189533577;
@@ -286,16 +294,23 @@ __global__ void __launch_bounds__(kMrThreads, kMrBlocks) mrope_append_kernel(con
   const int row0 = idx / a.Hkv * kMrVRows, g = idx % a.Hkv;
   const int n = min(kMrVRows, a.n_rows - row0);
   const bf16* src = a.qkv + row0 * a.qkv_ld + (a.Hq + a.Hkv + g) * D;
+  constexpr int kLoads = kMrVRows * (D / 8) / kMrThreads;  // 16-byte loads per thread, all on their way at once
+  uint4 v[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = i * kMrThreads + threadIdx.x, r = at / (D / 8);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < n) v[i] = *reinterpret_cast<const uint4*>(src + r * a.qkv_ld + at % (D / 8) * 8);
+  }
   if (threadIdx.x < kMrVRows) slot[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? slot_of(row0 + threadIdx.x) : -1;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n * (D / 8); i += kMrThreads) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    const uint4 v = *reinterpret_cast<const uint4*>(src + r * a.qkv_ld + c * 8);
-    uint32_t* d = reinterpret_cast<uint32_t*>(vt + r * kLd + c * 8);
-    d[0] = v.x;
-    d[1] = v.y;
-    d[2] = v.z;
-    d[3] = v.w;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = i * kMrThreads + threadIdx.x, r = at / (D / 8);
+    uint32_t* d = reinterpret_cast<uint32_t*>(vt + r * kLd + at % (D / 8) * 8);
+    d[0] = v[i].x;
+    d[1] = v[i].y;
+    d[2] = v[i].z;
+    d[3] = v[i].w;
   }
   __syncthreads();
   auto put = [&](int r, int d) {
@@ -307,29 +322,39 @@ __global__ void __launch_bounds__(kMrThreads, kMrBlocks) mrope_append_kernel(con
   // and the rows before r0, go one by one
   const int r0 = slot[0] >= 0 ? min(n, (8 - (slot[0] & 7)) & 7) : 0;
   for (int i = threadIdx.x; i < r0 * D; i += kMrThreads) put(i / D, i % D);
-  for (int i = threadIdx.x; i < kMrVRows / 8 * D; i += kMrThreads) {
-    // lanes: eight pieces next to one another (a 128-byte line of a page's feature row), then features
-    const int d = i >> 3, lo = r0 + (i & 7) * 8, hi = min(n, lo + 8);
-    if (lo >= hi) continue;
-    const int s0 = slot[lo];
-    bool run = hi - lo == 8 && s0 >= 0 && (s0 & 7) == 0;
-    if (run) {
+  // lanes: eight pieces next to one another (a 128-byte line of a page's
+  // feature row) of four feature pairs; a thread keeps its piece
+  constexpr int kPieces = kMrVRows / 8;
+  const int lo = r0 + static_cast<int>(threadIdx.x) % kPieces * 8, hi = min(n, lo + 8);
+  if (lo >= hi) return;
+  const int s0 = slot[lo];
+  bool run = hi - lo == 8 && s0 >= 0 && (s0 & 7) == 0;
+  if (run) {
 #pragma unroll
-      for (int e = 1; e < 8; ++e) run &= slot[lo + e] == s0 + e;
+    for (int e = 1; e < 8; ++e) run &= slot[lo + e] == s0 + e;
+  }
+  if (run) {
+    bf16* page = a.v_pages + (static_cast<size_t>(s0 >> 6) * a.Hkv + g) * D * 64 + (s0 & 63);
+#pragma unroll 4
+    for (int d2 = threadIdx.x / kPieces; d2 < D / 2; d2 += kMrThreads / kPieces) {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint32_t*>(vt + (lo + e) * kLd + 2 * d2);
+      uint4 even, odd;
+      even.x = __byte_perm(w[0], w[1], 0x5410);
+      even.y = __byte_perm(w[2], w[3], 0x5410);
+      even.z = __byte_perm(w[4], w[5], 0x5410);
+      even.w = __byte_perm(w[6], w[7], 0x5410);
+      odd.x = __byte_perm(w[0], w[1], 0x7632);
+      odd.y = __byte_perm(w[2], w[3], 0x7632);
+      odd.z = __byte_perm(w[4], w[5], 0x7632);
+      odd.w = __byte_perm(w[6], w[7], 0x7632);
+      *reinterpret_cast<uint4*>(page + 2 * d2 * 64) = even;
+      *reinterpret_cast<uint4*>(page + (2 * d2 + 1) * 64) = odd;
     }
-    if (run) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t x = *reinterpret_cast<const uint16_t*>(vt + (lo + 2 * e) * kLd + d);
-        const uint32_t y = *reinterpret_cast<const uint16_t*>(vt + (lo + 2 * e + 1) * kLd + d);
-        w[e] = x | (y << 16);
-      }
-      *reinterpret_cast<uint4*>(a.v_pages + ((static_cast<size_t>(s0 >> 6) * a.Hkv + g) * D + d) * 64 + (s0 & 63)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+  } else {
+    for (int d = threadIdx.x / kPieces; d < D; d += kMrThreads / kPieces)
       for (int r = lo; r < hi; ++r) put(r, d);
-    }
   }
 }
 
@@ -342,8 +367,7 @@ int head_groups(int n_rows, int heads) {
 }
 // Blocks for n_units warps of work, at most twice what the SMs hold at once
 // (a warp then takes two or three rows on one table of frequencies; once the
-// residents: 40 us, unlimited: 41 us, twice: 38.9 us for 16384 rows of 16/2
-// heads of 128).
+// residents: 37.7 us, twice: 35.9 us for 16384 rows of 16/2 heads of 128).
 int unit_blocks(long long n_units) {
   const long long b = (n_units + kMrWarps - 1) / kMrWarps, most = static_cast<long long>(device_sm_count()) * 2 * kMrBlocks;
   return static_cast<int>(b < most ? b : most);

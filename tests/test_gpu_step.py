@@ -158,7 +158,8 @@ ROPE_CASES = [
     # rows, heads, D, rot, sections, interleaved
     (1, 1, 2, 2, (1,), 0), (3, 5, 72, 72, (18, 18), 0), (33, 3, 80, 80, (20, 20), 1), (64, 2, 128, 128, (16, 24, 24), 0),
     (65, 4, 128, 128, (24, 20, 20), 1), (31, 7, 64, 32, (4, 6, 6), 0), (257, 1, 256, 256, (32, 32, 32, 32), 1),
-    (100, 3, 66, 30, (5, 5, 5), 0), (5, 70, 128, 64, (0, 32, 0), 0), (2000, 2, 64, 64, (32,), 0)]
+    (100, 3, 66, 30, (5, 5, 5), 0), (5, 70, 128, 64, (0, 32, 0), 0), (2000, 2, 64, 64, (32,), 0),
+    (6007, 2, 80, 80, (20, 20), 0), (12001, 1, 128, 64, (8, 12, 12), 1)]
 
 
 @pytest.mark.parametrize("rows,heads,D,rot,sections,interleaved", ROPE_CASES)
@@ -191,7 +192,8 @@ def test_mrope(cuda, rows, heads, D, rot, sections, interleaved, dtype):
 
 @pytest.mark.parametrize("rows,Hq,Hkv,D,sections,rot,interleaved", [
     (1, 16, 2, 128, (16, 24, 24), 0, 0), (16, 8, 1, 128, (24, 20, 20), 0, 1), (77, 14, 2, 64, (12, 10, 10), 0, 1),
-    (200, 3, 3, 64, (7, 8), 30, 0), (1030, 16, 2, 128, (64,), 0, 0)])
+    (200, 3, 3, 64, (7, 8), 30, 0), (1030, 16, 2, 128, (64,), 0, 0), (6100, 2, 1, 64, (12, 10, 10), 0, 0),
+    (12011, 2, 1, 128, (8, 12, 12), 64, 1)])
 def test_mrope_append(cuda, rows, Hq, Hkv, D, sections, rot, interleaved):
     rot = rot or D
     g = torch.Generator().manual_seed(rows)
