@@ -62,9 +62,12 @@ struct Piece<bf16> {
 __device__ __forceinline__ float as_f(float x) { return x; }
 __device__ __forceinline__ float as_f(bf16 x) { return __bfloat162float(x); }
 
-// max(p - q, 0); a NaN or infinite probability counts as nothing.
+// max(p - q, 0); a NaN or infinite probability counts as nothing.  One fp32
+// difference tells (a bit pattern between 0's and infinity's: positive and
+// finite); the value is the fp64 difference.
 __device__ __forceinline__ double residual(float p, float q) {
-  return (p > q && p < INFINITY) ? static_cast<double>(p) - static_cast<double>(q) : 0.0;
+  const uint32_t d = __float_as_uint(p - q);
+  return d - 1u < 0x7f7fffffu ? static_cast<double>(p) - static_cast<double>(q) : 0.0;
 }
 
 // N consecutive probabilities at v as loaded, 0 from hi on (kVec: hi is a
@@ -120,9 +123,9 @@ __global__ void __launch_bounds__(kSvThreads, 2) spec_sample_kernel(const SpecSa
         ok = x >= 0 && x < V;
         if (ok) {
           const size_t at = static_cast<size_t>(j) * V + x;
-          const double q = dp ? static_cast<double>(as_f(dp[at])) : 1.0;
-          ok = static_cast<double>(a.u_accept[static_cast<size_t>(seq) * K + j]) * q <
-               static_cast<double>(as_f(tp[at]));
+          const float p = as_f(tp[at]), q = dp ? as_f(dp[at]) : 1.f;
+          const double u = a.u_accept[static_cast<size_t>(seq) * K + j];
+          ok = u * q < p && fmaxf(fabsf(p), fabsf(q)) < INFINITY;
         } else if (rank == 0) {
           record_error(a.status, DVLM_ERR_BOUNDS);
         }
@@ -148,8 +151,8 @@ __global__ void __launch_bounds__(kSvThreads, 2) spec_sample_kernel(const SpecSa
   const int lo = static_cast<int>(lo_l < V ? lo_l : V);
   const int hi = static_cast<int>(min(lo_l + static_cast<long long>(per) * kStep, static_cast<long long>(V)));
 
-  // Residuals of the piece at v from its probabilities.  careful: NaN and
-  // infinities count as 0; else (no q) an infinity shows in the sum, NaN and
+  // Residuals of the piece at v from its probabilities.  With q, or careful:
+  // NaN and infinities count as 0; else an infinity shows in the sum, NaN and
   // negative values count as 0.
   auto values = [&](int v, bool careful, const Raw<T, kVec>& wp, const Raw<T, kVec>& wq, double (&r)[N]) {
     float fp[N];

@@ -404,8 +404,9 @@ DVLM_API dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void*
  * [b, K + 1] int32.  When cache_len (device int32 [b], slots after the
  * verify pass wrote the n_draft rows) and cache_len_out are given, the latter
  * receives cache_len - (n_draft - k): the cache cut back to the accepted rows;
- * it may be the same array.  Rows need not sum to 1.  NaN and infinite
- * probabilities count as 0 in a draw and refuse a draft.  u_sample outside
+ * it may be the same array.  Rows need not sum to 1.  A token whose target or
+ * draft probability is NaN or infinite counts as 0 in a draw and is refused as
+ * a draft.  u_sample outside
  * [0, 1) counts as the nearest value inside.  If r is 0 everywhere the draw is
  * from the target row itself; if that is 0 too, token 0 and DVLM_ERR_BOUNDS.
  * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS), as is an n_draft

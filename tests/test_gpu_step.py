@@ -365,3 +365,28 @@ def test_verify_draws_the_target(cuda):
         got += float(q[x]) * np.bincount(out[:, 0], minlength=V) / b
     # each token's share: an acceptance step and V sampling steps of the lattice, each within 1/n
     assert np.abs(got - p.numpy()).max() <= 2.0 / n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_verify_infinite_drafts(cuda, dtype):
+    """NaN and infinities of either sign in the draft's or the target's row: no such token is accepted or drawn, and
+    every sequence gets its token."""
+    V, K, inf = 2560, 1, float("inf")
+    p = torch.zeros(6, K + 1, V)
+    p[:, :, 40:48] = 0.125
+    q = torch.zeros(6, K, V)
+    q[:, :, 40] = 0.5
+    ids = np.full((6, K), 40, dtype=np.int64)
+    us = np.array([0.0, 0.5, 0.99, 0.0, 0.5, 0.99], dtype=np.float32)
+    q[0:3, :, 41] = -inf                                    # p - q would be infinite
+    q[0:3, :, 42], q[0:3, :, 43] = inf, float("nan")
+    p[3:6, :, 41], p[3:6, :, 42], p[3:6, :, 43] = -inf, inf, float("nan")
+    acc, out, _, st = run_verify(cuda, p.to(dtype), q.to(dtype), ids, np.ones((6, K)), us)
+    assert st == 0 and (acc == 0).all()
+    assert out[:, 0].tolist() == [44, 46, 47, 44, 46, 47]   # 44 .. 47 are left, a quarter each
+    # as drafts: u = 0 accepts whatever has a finite probability, and only that
+    for tok, ok in ((41, 0), (42, 0), (43, 0), (45, 1)):
+        ids[:] = tok
+        acc, out, _, st = run_verify(cuda, p.to(dtype), q.to(dtype), ids, np.zeros((6, K)), us)
+        assert st == 0 and acc.tolist() == [ok] * 6
+        assert ok or set(out[:, 0].tolist()) <= {40, 44, 45, 46, 47}
