@@ -435,7 +435,8 @@ dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int
       !free_count_out)
     return DVLM_ERR_INVALID_ARG;
   if (n_batch < 1 || n_batch > kPlanMaxBatch || max_pages < 1 || max_pages > kMaxPages || n_pages < 1 ||
-      n_pages > kMaxPages || max_rows < 1)
+      n_pages > kMaxPages || max_rows < 1 || max_rows > (1 << 30) ||
+      static_cast<long long>(n_batch) * max_pages > 0x7fffffffLL)
     return DVLM_ERR_SHAPE;
   PagePlanArgs a{cache_len, new_len, block_table, free_pages, free_count, n_batch, max_pages, n_pages, max_rows,
                  kv_len, cu_rows, slot_map, free_count_out, held_len,
@@ -498,8 +499,10 @@ dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void* k_pages,
                                   float scale, void* workspace, size_t ws_bytes, int* dev_status,
                                   dvlm_stream stream) {
   if (!q || !out || !k_pages || !v_pages || !block_table || !kv_len || !cu_rows) return DVLM_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return DVLM_ERR_INVALID_ARG;
-  if (n_batch < 1 || n_rows < 1 || n_pages < 1 || n_pages > kMaxPages || max_pages < 1 || max_pages > kMaxPages ||
+  const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2) || !(scale_log2 > 0.f)) return DVLM_ERR_INVALID_ARG;
+  if (n_batch < 1 || n_batch > (1 << 24) || n_rows < 1 || n_rows > (1 << 30) || n_pages < 1 || n_pages > kMaxPages ||
+      max_pages < 1 || max_pages > kMaxPages ||
       Hq < 1 || Hkv < 1 || Hq > 4096 || D < 1 || Hq % Hkv)
     return DVLM_ERR_SHAPE;
   // page rows are TMA coordinates: n_pages * Hkv * max(64, D) stays in 31 bits
@@ -532,7 +535,7 @@ dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void* k_pages,
   a.max_pages = max_pages;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.workspace = workspace;
   a.status = dev_status;
   return cuda_status(launch_attn_chunk(mq, mk, mv, a, D, P, cs(stream)));

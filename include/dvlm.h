@@ -297,15 +297,17 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * free_count_out [1].  held_len [n_batch] (in/out, may be NULL): slots whose
  * pages a request still holds where its cache was cut back behind its last
  * step (dvlm_spec_verify_sample); the plan then counts ceil(max(held_len,
- * cache_len) / 64) pages as held, and sets it to the larger of itself and
+ * cache_len) / 64) pages as held (one below cache_len, negative ones too, counts
+ * as cache_len), and sets it to the larger of itself and
  * kv_len (0 for a finished request).  kv_len may be cache_len and
- * free_count_out may be free_count; no other arrays may overlap.  A request whose cached or held
- * length is outside 0 .. 64 max_pages, whose new length is below -1, or whose sum is
+ * free_count_out may be free_count; no other arrays may overlap.  A request whose cached
+ * length is outside 0 .. 64 max_pages, whose held length is above that, whose new length is below -1, or whose sum is
  * past 64 max_pages takes no part (kv_len: 0 in the first two cases, its
  * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
  * numbers are passed on as they are.  All pointers device int32.  n_batch <=
- * 4096, n_pages and max_pages < 2^25.  Errors: INVALID_ARG, SHAPE.  One
+ * 4096, n_pages and max_pages < 2^25, n_batch * max_pages < 2^31, max_rows <=
+ * 2^30.  Errors: INVALID_ARG, SHAPE.  One
  * launch, no workspace. */
 DVLM_API dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
                                    int32_t* free_pages, const int32_t* free_count, int n_batch, int max_pages,
@@ -367,7 +369,8 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
  * q.k_j), -inf for such a row.  Rows before cu_rows[0] or behind
  * cu_rows[n_batch] are left as they are.  Pages as in dvlm_block_attn_paged,
  * with D == 64 or 128 and 1 <= Hq / Hkv <= 128; the page stores' rows
- * (n_pages * Hkv * max(D, 64)) stay below 2^31.  scale > 0.  Hidden slots and
+ * (n_pages * Hkv * max(D, 64)) stay below 2^31; n_batch <= 2^24, n_rows <= 2^30.
+ * scale > 0 (scale * log2(e) a finite fp32).  Hidden slots and
  * those at or beyond kv_len[b] may hold anything, NaN included; the slots
  * between must be finite.  Scores, softmax and sums in fp32, P in bf16.  The
  * result of a row depends on the other requests of the call only in the

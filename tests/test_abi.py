@@ -285,3 +285,20 @@ def test_chunk_attention_host_validation(dvlm_lib):
     assert dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 96) == 0
     assert dv.chunk_attn_paged_workspace_size(0, 1, 16, 2, 128) == 0
     assert 0 < dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 64) < dv.chunk_attn_paged_workspace_size(1, 1, 16, 2, 128)
+
+
+def test_step_limits(dvlm_lib):
+    """Sizes whose offsets or counts would pass what the kernels hold in 31 bits."""
+    assert _plan(rows=(1 << 30) + 1) == SHAPE and _plan(rows=2 ** 31 - 1) == SHAPE
+    assert _plan(n=4096, mp=1 << 20) == SHAPE
+
+    def chunk(n=1, rows=4, scale=0.1, ws=16, ws_bytes=0):
+        return dv.lib().dvlm_chunk_attn_paged(16, 16, 16, 16, 16, 16, 16, None, None, None, n, rows, 4, 8, 8, 2, 64, 512,
+                                              scale, ws, ws_bytes, None, None)
+    assert chunk() == WORKSPACE
+    for n in ((1 << 24) + 1, 2 ** 31 - 1):
+        assert chunk(n=n) == SHAPE
+    for rows in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert chunk(rows=rows) == SHAPE
+    for scale in (3e38, 1e-46, 0.0, -1.0, float("inf"), float("nan")):
+        assert chunk(scale=scale) == INVALID
