@@ -62,7 +62,7 @@ struct AcCfg {
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kQ;
   static constexpr int oBar = oKV + kStages * kStage;
-  static constexpr int kBars = 2 * kAcRing + 2 + 2 * kStages + 4 + 4 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kAcRing + 2 + 2 * kStages + 4 + 4 + 2 + 2 + 1 + 1;
   static constexpr int oDesc = oBar + 512;
   static constexpr int oML = oDesc + kAcRing * 64;
   static constexpr int kSmem = oML + 2 * 128 * 8 + 1024;
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   uint64_t* pv_done = p_full + 4;          // [2] P V of a page done (one phase per page)
   uint64_t* o_done = pv_done + 2;          // [2] last P V of the item done (pv_done may be two phases behind there)
   uint64_t* x_bar = o_done + 2;            // the softmax warps of both tiles meet (a bounded wait, unlike bar.sync)
+  uint64_t* mma_idle = x_bar + 1;          // every product of this CTA done
   static_assert(C::kBars * 8 + 16 <= 512, "barrier space");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* sabort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -408,6 +409,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return wait_longer(bar, parity, a.status, sabort);
+  };
+  // the same where nothing hangs on the outcome and another wait has perhaps given up
+  auto warp_wait_only = [&](uint64_t* bar, uint32_t parity) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) wait_longer(bar, parity, a.status, nullptr);
   };
 
   if (warp == 0) {
@@ -561,6 +566,9 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         mbar_arrive(&d_full[slot]);
       }
     }
+    // no copy is on its way into this CTA's memory when it ends, after a wait that gave up either
+    for (int p = max(0, pos - NS); p < pos; ++p) warp_wait_only(&kv_full[p % NS], (p / NS) & 1);
+    if (nq > 0) warp_wait_only(q_full, (nq - 1) & 1);
     // merge record: the item this CTA began and did not finish
     if (lane == 0) {
       int* rec = ws.rec + cta * 16;
@@ -657,6 +665,9 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         }
         if (ok) mbar_arrive(&d_empty[slot]);
       }
+      // nor a product under way when its TMEM is given back
+      umma_commit(mma_idle);
+      mbar_wait(mma_idle, 0, a.status, nullptr);
     }
   } else {
     // ------------------------------------------------ softmax and output
