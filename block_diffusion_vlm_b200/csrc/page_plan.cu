@@ -29,6 +29,7 @@ constexpr int kPlanPer = kPlanMaxBatch / kPlanThreads;  // requests per thread o
 constexpr int kPlanCtas = 8;
 constexpr int kPlanWide = 4096;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanNoPage = (1 << 25) - 1;  // past every store; its slot numbers still fit 31 bits
 
 // Inclusive scan over the warp.
 __device__ __forceinline__ long long warp_scan(long long v, int lane) {
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
         const int slot = s_cache[b] + (i + e - s_row[b]), p = slot >> 6, held = s_held[b];
         if (p != last) {
           page = p < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + p] : taken(s_need[b] + p - held);
+          page = max(-kPlanNoPage, min(page, kPlanNoPage));  // (a wild number's slots must not wrap into the store)
           last = p;
         }
         v[e] = page * 64 + (slot & 63);

@@ -305,7 +305,8 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * past 64 max_pages takes no part (kv_len: 0 in the first two cases, its
  * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
- * numbers are passed on as they are.  All pointers device int32.  n_batch <=
+ * numbers are passed on as they are (in slot_map cut to +- (2^25 - 1), past any
+ * store).  All pointers device int32.  n_batch <=
  * 4096, n_pages and max_pages < 2^25, n_batch * max_pages < 2^31, max_rows <=
  * 2^30.  Errors: INVALID_ARG, SHAPE.  One
  * launch, no workspace. */
@@ -379,6 +380,7 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
  * max_pages or below n_b, takes no part (DVLM_ERR_BOUNDS); a page number
  * outside 0 .. n_pages - 1 sets DVLM_ERR_BOUNDS and page 0 is read.  cu_rows,
  * kv_len, n_noisy, n_hidden, block_table [n_batch, max_pages]: device int32.
+ * out, lse, the inputs and the workspace must not overlap.
  * workspace: dvlm_chunk_attn_paged_workspace_size bytes (device, 16-byte
  * aligned, any contents; about 39 MB at D = 128); calls sharing one must not
  * overlap.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED (other head shapes),

@@ -390,3 +390,22 @@ def test_verify_infinite_drafts(cuda, dtype):
         acc, out, _, st = run_verify(cuda, p.to(dtype), q.to(dtype), ids, np.zeros((6, K)), us)
         assert st == 0 and acc.tolist() == [ok] * 6
         assert ok or set(out[:, 0].tolist()) <= {40, 44, 45, 46, 47}
+
+
+def test_page_plan_wild_pages(cuda):
+    """Page numbers whose slots would wrap around 32 bits into the store give slots outside it."""
+    wild = [2 ** 26 + 1, 2 ** 31 - 1, -2 ** 31, -2 ** 26 + 2, 2 ** 25, -2 ** 25 - 1]
+    n = len(wild)
+    table = np.full((n, 2), -1, dtype=np.int32)
+    table[:, 0] = wild
+    kv, cu, slots, tab, free, count, st, _ = run_plan(cuda, [5] * n, [3] * n, table, [], 4, 3 * n + 2)
+    assert kv.tolist() == [8] * n and cu.tolist() == [3 * i for i in range(n + 1)]
+    assert (tab == table).all() and int(count[0]) == 0
+    for i, page in enumerate(wild):
+        got = slots[3 * i:3 * i + 3].astype(np.int64)
+        assert ((got >= 4 * 64) if page > 0 else (got < -1)).all()
+        assert (got % 64 == [5, 6, 7]).all()
+    assert slots[3 * n:].tolist() == [-1, -1]
+    # a stack's wild number reaches the table as it is
+    kv, cu, slots, tab, free, count, st, _ = run_plan(cuda, [0], [2], np.full((1, 1), -1, dtype=np.int32), [2 ** 27], 4, 2)
+    assert tab.tolist() == [[2 ** 27]] and (slots >= 4 * 64).all()
