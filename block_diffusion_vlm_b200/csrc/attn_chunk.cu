@@ -51,6 +51,7 @@ constexpr int kAcThreads = 320;  // warp 0 loads and schedules, 1 issues MMAs, 2
 constexpr int kAcKeys = 64;      // slots per step: one page
 constexpr int kAcRing = 4;       // work descriptors in flight
 constexpr int kAcItemCost = 320; // fixed cost of an item, in slot units (prologue and epilogue: 4300 cycles, a slot of a tile 14.5)
+constexpr int kAcLongPart = 1024; // parts from here on count an item's fixed cost in full where it begins
 constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
@@ -463,30 +464,44 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const int te = k.t0 + k.ntok, end = te > r.nclean ? r.kv : r.base + te;
         const int cb = r.hid / kAcKeys, nch = end > r.hid ? (end + kAcKeys - 1) / kAcKeys - cb : 0;
         // the part's pages; a solo item is cut between pairs of pages (the CTA
-        // that ends here and the one that goes on compute the same cut)
+        // that ends here and the one that goes on compute the same cut).  Long
+        // parts: the item's fixed cost comes first, then 128 units a page or
+        // pair of pages, so that a CTA that begins an item has paid for it;
+        // short ones: pages in proportion, so that few rows spread evenly.
         const int unit = solo ? 2 : 1;
         const int nu = (nch + unit - 1) / unit;
         const float scale = __fdividef(static_cast<float>(nu), static_cast<float>(w));
-        const int ca = min(nu, static_cast<int>(static_cast<float>(xa) * scale)) * unit;
-        const int ce = xb == w ? nch : min(nu, static_cast<int>(static_cast<float>(xb) * scale)) * unit;
+        auto pages_before = [&](long long y) -> int {
+          if (y >= w) return nch;
+          const long long u = share >= kAcLongPart ? max(0LL, y - kAcItemCost + kAcKeys) >> 7
+                                                   : static_cast<long long>(static_cast<float>(y) * scale);
+          return min(nch, static_cast<int>(min(u, static_cast<long long>(nu))) * unit);
+        };
+        const int ca = pages_before(xa), ce = pages_before(xb);
+        // an item belongs to the CTAs that hold pages of it (without any: to the one that holds its first unit)
+        const bool begins = ca == 0, ends = ce == nch;
+        const bool take = nch == 0 ? xa == 0 : !(begins && ce == 0) && ca < nch;
         k.c0 = cb + ca;
-        k.nc = max(0, min(ce, nch) - min(ca, nch));
-        k.slot = (xa == 0 && xb == w) ? -1 : (xa == 0 ? 1 : 0);
-        if (k.slot == 1) {  // the item goes on: the CTA that holds its last unit
+        k.nc = ce - ca;
+        k.slot = begins && ends ? -1 : begins ? 1 : 0;
+        if (take && k.slot == 1) {  // the item goes on: the CTA that holds its last pages
           rec_kind = k.kind;
           rw = k;
           rec_last = div_small(start + w - 1, share);
+          while (pages_before(rec_last * share - start) >= nch) --rec_last;
         }
         // hand the descriptor over
-        const int slot = it % kAcRing;
-        if (it >= kAcRing) ok = warp_wait(&d_empty[slot], ((it / kAcRing) - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          desc[slot] = k;
-          mbar_arrive(&d_full[slot]);
+        if (take) {
+          const int slot = it % kAcRing;
+          if (it >= kAcRing) ok = warp_wait(&d_empty[slot], ((it / kAcRing) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            desc[slot] = k;
+            mbar_arrive(&d_full[slot]);
+          }
+          ++it;
         }
-        ++it;
-        if (k.nc > 0) {
+        if (take && k.nc > 0) {
           // Q: rows [row0, +tpt) (and the next tpt for a pair) of the KV head's query heads
           if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1);
           if (!ok) break;
@@ -828,12 +843,19 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float f = k.slot < 0 ? inv : 1.f;
 #pragma unroll 1
-        for (int cc = 0; live && cc < D; cc += 16) {
-          float x[16];
-          tmem_ld16(tO + cc, x);
+        for (int cc = 0; live && cc < D; cc += 64) {
+          uint32_t u[2][32];
+          tmem_ld32_nowait(tO + cc, u[0]);
+          tmem_ld32_nowait(tO + cc + 32, u[1]);
+          tmem_wait_ld32(u[0]);
+          tmem_wait_ld32(u[1]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = k.nc > 0 && l > 0.f ? x[j] * f : 0.f;
-          store_cols(k, tok, valid, w, cc, x);
+          for (int h = 0; h < 4; ++h) {
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = k.nc > 0 && l > 0.f ? __uint_as_float(u[h >> 1][(h & 1) * 16 + j]) * f : 0.f;
+            store_cols(k, tok, valid, w, cc + h * 16, x);
+          }
         }
         if (valid) {
           if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + w * 128 + row] = make_float2(m, l);
