@@ -269,6 +269,23 @@ def selftest_wait_timeout(budget_cycles: int, status, gave_up, stream=None) -> N
 
 
 # ---------------------------------------------------------------- batched step over paged caches
+_numel = None  # torch's queries of a tensor, as functions (set by _bind_torch)
+
+
+def _bind_torch() -> None:
+    """Look torch's queries up once: a call asks four of each of its ten tensors, and the lookups of
+    methods and modules took a third of a small call's time."""
+    import torch
+    global _numel, _gpu_of, _dense, _address, _raw_stream, _current_gpu, _i32, _f32, _bf16
+    _i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
+    _gpu_of, _dense, _address = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+    # (the direct queries where this torch has them: the stream object costs a microsecond)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _numel = torch.Tensor.numel
+
+
 def _take(where: str, dev: int, *args) -> list:
     """Device addresses of tensors, refusing those the library would misread: args are (tensor, dtype,
     least number of elements) triples; all contiguous, all on GPU number dev.  None stays None."""
@@ -276,8 +293,8 @@ def _take(where: str, dev: int, *args) -> list:
     for t, dtype, least in args:
         if t is None:
             out.append(None)
-        elif t.dtype is dtype and t.numel() >= least and t.get_device() == dev and t.is_contiguous():
-            out.append(t.data_ptr())
+        elif t.dtype is dtype and _numel(t) >= least and _gpu_of(t) == dev and _dense(t):
+            out.append(_address(t))
         else:
             raise DvlmError(1, f"{where}: expected a contiguous {dtype} tensor of at least {least} elements on "
                                f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -286,31 +303,25 @@ def _take(where: str, dev: int, *args) -> list:
 
 def _device(where: str, t) -> int:
     """GPU number of a call's first tensor."""
-    dev = t.get_device()
+    if _numel is None:
+        _bind_torch()
+    dev = _gpu_of(t)
     if dev < 0:
         raise DvlmError(1, f"{where}: the tensors are on {t.device}, not on a GPU")
     return dev
 
 
-def _raw_stream(dev: int) -> int:
-    """Handle of torch's current stream on a GPU (the direct query where this torch has it: the
-    stream object costs a microsecond, a sixth of a small call)."""
-    import torch
-    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return query(dev) if query is not None else torch.cuda.current_stream(dev).cuda_stream
-
-
 def _launch(fn, where: str, dev: int, stream, *args) -> None:
     """Call an entry point whose last argument is the stream, with GPU dev
     current (a NULL stream is torch's current one on that GPU)."""
-    import torch
     if stream is None:
         stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_gpu():
         status = fn(*args, stream)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = fn(*args, stream)
     if status != 0:
@@ -332,8 +343,7 @@ def _sections(sections):
 def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batch, max_pages, n_pages, max_rows,
               kv_len, cu_rows, slot_map, free_count_out, held_len=None, status=None, stream=None) -> None:
     """Block tables, row offsets and slot map of a ragged step (dvlm_page_plan)."""
-    import torch
-    i32, dev = torch.int32, _device("dvlm_page_plan", cache_len)
+    dev, i32 = _device("dvlm_page_plan", cache_len), _i32
     p = _take("dvlm_page_plan", dev, (cache_len, i32, n_batch), (new_len, i32, n_batch),
               (block_table, i32, n_batch * max_pages), (free_pages, i32, n_pages), (free_count, i32, 1),
               (kv_len, i32, n_batch), (cu_rows, i32, n_batch + 1), (slot_map, i32, max_rows), (free_count_out, i32, 1),
@@ -344,14 +354,15 @@ def page_plan(cache_len, new_len, block_table, free_pages, free_count, *, n_batc
 def _rows(where: str, t, dtype, rows: int, ld: int, width: int, dev: int) -> int:
     """Row stride (elements) of a tensor whose rows of `width` elements lie ld apart.  0: the tensor's
     own first stride, its leading index counting the rows, or width for a dense tensor."""
-    if t.dtype is not dtype or t.get_device() != dev:
+    if t.dtype is not dtype or _gpu_of(t) != dev:
         raise DvlmError(1, f"{where}: expected a {dtype} tensor on cuda:{dev}, got {t.dtype} on {t.device}")
     if rows < 1:
         return ld or width  # (the library refuses the call)
-    if t.is_contiguous():
+    if _dense(t):
+        n = _numel(t)
         if not ld:
-            ld = t.numel() // t.shape[0] if t.dim() > 1 and t.shape[0] >= rows and t.numel() >= rows * width else width
-        if t.numel() >= (rows - 1) * ld + width:
+            ld = n // t.shape[0] if t.dim() > 1 and t.shape[0] >= rows and n >= rows * width else width
+        if n >= (rows - 1) * ld + width:
             return ld
     elif not ld and t.dim() > 1 and t.shape[0] >= rows and t[0].numel() >= width and t[0].is_contiguous():
         return t.stride(0)
@@ -363,27 +374,26 @@ def mrope(x, out, pos, *, n_rows, n_heads, D, sections, rope_base, dtype, rot_di
           status=None, stream=None) -> None:
     """Rotary positions with len(sections) axes on rows of heads (dvlm_mrope).  rot_dim 0: D.
     Row strides 0: taken from the tensors (rows may be slices of wider rows)."""
-    import torch
-    dev, td = _device("dvlm_mrope", x), torch.float32 if dtype == DVLM_FP32 else torch.bfloat16
+    dev = _device("dvlm_mrope", x)
+    td = _f32 if dtype == DVLM_FP32 else _bf16
     x_ld = _rows("dvlm_mrope", x, td, n_rows, x_ld, n_heads * D, dev)
     out_ld = _rows("dvlm_mrope", out, td, n_rows, out_ld, n_heads * D, dev)
     sec = _sections(sections)
-    p = _take("dvlm_mrope", dev, (pos, torch.int32, len(sec) * n_rows), (status, torch.int32, 1))
-    _launch(lib().dvlm_mrope, "dvlm_mrope", dev, stream, x.data_ptr(), out.data_ptr(), p[0], n_rows, n_heads, D, x_ld,
+    p = _take("dvlm_mrope", dev, (pos, _i32, len(sec) * n_rows), (status, _i32, 1))
+    _launch(lib().dvlm_mrope, "dvlm_mrope", dev, stream, _address(x), _address(out), p[0], n_rows, n_heads, D, x_ld,
             out_ld, rot_dim or D, len(sec), sec, rope_base, interleaved, dtype, p[1])
 
 
 def mrope_append_paged(qkv, pos, slot_map, q_out, k_pages, v_pages, *, n_rows, Hq, Hkv, D, n_pages, sections,
                        rope_base, rot_dim=0, interleaved=0, qkv_ld=0, status=None, stream=None) -> None:
     """Rotate queries and keys and write keys and values into their pages (dvlm_mrope_append_paged)."""
-    import torch
-    dev, bf = _device("dvlm_mrope_append_paged", qkv), torch.bfloat16
+    dev, bf = _device("dvlm_mrope_append_paged", qkv), _bf16
     qkv_ld = _rows("dvlm_mrope_append_paged", qkv, bf, n_rows, qkv_ld, (Hq + 2 * Hkv) * D, dev)
     sec = _sections(sections)
-    p = _take("dvlm_mrope_append_paged", dev, (pos, torch.int32, len(sec) * n_rows), (slot_map, torch.int32, n_rows),
+    p = _take("dvlm_mrope_append_paged", dev, (pos, _i32, len(sec) * n_rows), (slot_map, _i32, n_rows),
               (q_out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
-              (v_pages, bf, n_pages * Hkv * 64 * D), (status, torch.int32, 1))
-    _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, qkv.data_ptr(), *p[:5], n_rows, Hq,
+              (v_pages, bf, n_pages * Hkv * 64 * D), (status, _i32, 1))
+    _launch(lib().dvlm_mrope_append_paged, "dvlm_mrope_append_paged", dev, stream, _address(qkv), *p[:5], n_rows, Hq,
             Hkv, D, n_pages, qkv_ld, rot_dim or D, len(sec), sec, rope_base, interleaved, p[5])
 
 
@@ -395,23 +405,21 @@ def chunk_attn_paged(q, out, k_pages, v_pages, block_table, kv_len, cu_rows, *, 
                      Hq, Hkv, D, scale, workspace, n_noisy=None, n_hidden=None, lse=None, q_ld=0, status=None,
                      stream=None) -> None:
     """Attention of ragged chunks of rows over paged caches (dvlm_chunk_attn_paged)."""
-    import torch
-    dev, bf, i32 = _device("dvlm_chunk_attn_paged", q), torch.bfloat16, torch.int32
+    dev, bf, i32 = _device("dvlm_chunk_attn_paged", q), _bf16, _i32
     q_ld = _rows("dvlm_chunk_attn_paged", q, bf, n_rows, q_ld, Hq * D, dev)
     p = _take("dvlm_chunk_attn_paged", dev, (out, bf, n_rows * Hq * D), (k_pages, bf, n_pages * Hkv * 64 * D),
               (v_pages, bf, n_pages * Hkv * 64 * D), (block_table, i32, n_batch * max_pages), (kv_len, i32, n_batch),
               (cu_rows, i32, n_batch + 1), (n_noisy, i32, n_batch), (n_hidden, i32, n_batch),
-              (lse, torch.float32, n_rows * Hq), (workspace, workspace.dtype, 0), (status, i32, 1))
-    _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, q.data_ptr(), *p[:9], n_batch, n_rows,
-            n_pages, max_pages, Hq, Hkv, D, q_ld, scale, p[9], workspace.numel() * workspace.element_size(), p[10])
+              (lse, _f32, n_rows * Hq), (workspace, workspace.dtype, 0), (status, i32, 1))
+    _launch(lib().dvlm_chunk_attn_paged, "dvlm_chunk_attn_paged", dev, stream, _address(q), *p[:9], n_batch, n_rows,
+            n_pages, max_pages, Hq, Hkv, D, q_ld, scale, p[9], _numel(workspace) * workspace.element_size(), p[10])
 
 
 def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K, V, dtype, accept_len, out_ids,
                        n_draft=None, cache_len=None, cache_len_out=None, status=None, stream=None) -> None:
     """Verify drafts by rejection sampling with given random numbers (dvlm_spec_verify_sample)."""
-    import torch
-    dev, i32, f32 = _device("dvlm_spec_verify_sample", target_p), torch.int32, torch.float32
-    td = f32 if dtype == DVLM_FP32 else torch.bfloat16
+    dev, i32, f32 = _device("dvlm_spec_verify_sample", target_p), _i32, _f32
+    td = f32 if dtype == DVLM_FP32 else _bf16
     p = _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
               (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),
               (accept_len, i32, b), (out_ids, i32, b * (K + 1)), (cache_len, i32, b), (cache_len_out, i32, b),
