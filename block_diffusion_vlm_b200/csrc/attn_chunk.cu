@@ -26,13 +26,14 @@
 // Bound and measure: a page of a pair item takes about 2100 cycles, of which
 // the exponentials of its 256 x 64 scores hold their unit for 1024 and the
 // products the tensor pipe for 1260; chunks of rows run into the 1000 W power
-// cap (1.74 of 1.965 GHz).  4096 rows over 12288 slots, 16/2 heads of 128: 335
-// us, 1.03 PFLOP/s.  Steps of two pages with one score buffer: 340 to 366 us
+// cap (1.74 of 1.965 GHz).  4096 rows over 12288 slots, 16/2 heads of 128: 332
+// us, 1.04 PFLOP/s.  Steps of two pages with one score buffer: 340 to 366 us
 // (the scores' latency stands between two steps); four warpgroups with the
 // keys of a page halved between two: 352 us, and with a second issuing thread
 // 350 us at lower clocks; a quarter or half of the exponentials as a
 // polynomial on the multiply-add pipe: 343 and 355 us.  64 single tokens over
-// 900 to 16000 slots read 5.6 TB/s (90 us).
+// 900 to 16000 slots read 5.9 TB/s (86 us; 94 us after a second of nothing
+// else, at the power cap and 1.6 GHz).
 //
 // Work split: all (request, KV head, pair or solo item) are laid end to end by
 // their cost in slots, and the line is cut into equal parts, one per CTA (one
@@ -51,7 +52,6 @@ constexpr int kAcThreads = 320;  // warp 0 loads and schedules, 1 issues MMAs, 2
 constexpr int kAcKeys = 64;      // slots per step: one page
 constexpr int kAcRing = 4;       // work descriptors in flight
 constexpr int kAcItemCost = 320; // fixed cost of an item, in slot units (prologue and epilogue: 4300 cycles, a slot of a tile 14.5)
-constexpr int kAcLongPart = 1024; // parts from here on count an item's fixed cost in full where it begins
 constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
@@ -463,19 +463,16 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         k.g = g;
         const int te = k.t0 + k.ntok, end = te > r.nclean ? r.kv : r.base + te;
         const int cb = r.hid / kAcKeys, nch = end > r.hid ? (end + kAcKeys - 1) / kAcKeys - cb : 0;
-        // the part's pages; a solo item is cut between pairs of pages (the CTA
-        // that ends here and the one that goes on compute the same cut).  Long
-        // parts: the item's fixed cost comes first, then 128 units a page or
-        // pair of pages, so that a CTA that begins an item has paid for it;
-        // short ones: pages in proportion, so that few rows spread evenly.
-        const int unit = solo ? 2 : 1;
-        const int nu = (nch + unit - 1) / unit;
-        const float scale = __fdividef(static_cast<float>(nu), static_cast<float>(w));
+        // the part's pages (the CTA that ends here and the one that goes on
+        // compute the same cut): the item's fixed cost comes first, so that a
+        // CTA that begins an item has paid for it, then 128 units a page, or
+        // pair of pages of a solo item (the fixed cost spread over the pages
+        // left CTAs with many short items a fifth behind the others: 24 mixed
+        // requests 31 us, against 29; 2 blocks of 16 rows 15.4, against 13.3)
         auto pages_before = [&](long long y) -> int {
           if (y >= w) return nch;
-          const long long u = share >= kAcLongPart ? max(0LL, y - kAcItemCost + kAcKeys) >> 7
-                                                   : static_cast<long long>(static_cast<float>(y) * scale);
-          return min(nch, static_cast<int>(min(u, static_cast<long long>(nu))) * unit);
+          const int u = static_cast<int>(max(0LL, y - kAcItemCost + kAcKeys) >> 7);
+          return min(nch, solo ? 2 * u : u);
         };
         const int ca = pages_before(xa), ce = pages_before(xb);
         // an item belongs to the CTAs that hold pages of it (without any: to the one that holds its first unit)
