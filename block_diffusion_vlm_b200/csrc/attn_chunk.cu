@@ -32,8 +32,8 @@
 // keys of a page halved between two: 352 us, and with a second issuing thread
 // 350 us at lower clocks; a quarter or half of the exponentials as a
 // polynomial on the multiply-add pipe: 343 and 355 us.  64 single tokens over
-// 900 to 16000 slots read 5.9 TB/s (86 us; 94 us after a second of nothing
-// else, at the power cap and 1.6 GHz).
+// 900 to 16000 slots read 5.9 TB/s (86 us; 91 us after a second of nothing
+// else, at the power cap and 1.65 GHz).
 //
 // Work split: all (request, KV head, pair or solo item) are laid end to end by
 // their cost in slots, and the line is cut into equal parts, one per CTA (one
@@ -69,6 +69,8 @@ struct AcCfg {
   static constexpr int kSmem = oML + 2 * 128 * 8 + 1024;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kAcKeys);
   static constexpr uint32_t kIdescO = idesc_bf16_f32(128, D);
+  static constexpr uint32_t kIdescS64 = idesc_bf16_f32(64, kAcKeys);  // products of thin items
+  static constexpr uint32_t kIdescO64 = idesc_bf16_f32(64, D);
 };
 constexpr uint32_t kAcColO = 256;
 
@@ -609,7 +611,12 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           mbar_arrive(&d_empty[slot]);
           continue;
         }
-        const bool solo = kind == 2;
+        // Up to 16 lanes of rows (single tokens): products of 64 rows instead of
+        // 128, whose first 16 lie in the same lanes.  The same time at full
+        // clocks, but half the tensor pipe's work at the power cap: 64 tokens
+        // over 900 to 16000 slots again and again, 99 us against 91
+        const bool solo = kind == 2, thin = solo && desc[slot].ntok * G <= 16;
+        const uint32_t id_s = thin ? C::kIdescS64 : C::kIdescS, id_o = thin ? C::kIdescO64 : C::kIdescO;
         ok = mbar_wait(q_full, nq & 1, a.status, sabort);
         if (!ok) break;
         ++nq;
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             umma_bf16_ss(tmem + w * 128 + buf * 64, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                         kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+                         kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
           umma_commit(&s_full[w * 2 + buf]);
         };
         auto issue_pv = [&](int w, int st, bool first, bool last) -> bool {
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           const uint64_t vd = kd0 + ((st * C::kStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tmem + kAcColO + w * D, tmem + w * 128 + buf * 64 + kk * 8, vd + ((kk * 32) >> 4), C::kIdescO,
+            umma_f16_ts(tmem + kAcColO + w * D, tmem + w * 128 + buf * 64 + kk * 8, vd + ((kk * 32) >> 4), id_o,
                         (!first || kk > 0) ? 1u : 0u);
           umma_commit(&pv_done[w]);
           if (last) umma_commit(&o_done[w]);

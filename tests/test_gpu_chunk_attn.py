@@ -226,3 +226,20 @@ def test_bad_requests_take_no_part(cuda):
             c["reqs"] = full[:3]
         c["rows"] = out.shape[0]
         check(c, out, lse, rows_of=good)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,Hkv,n", [(16, 1, 1), (15, 2, 1), (17, 1, 1), (8, 2, 2), (8, 1, 3), (1, 3, 16), (1, 2, 17),
+                                     (5, 2, 3), (5, 2, 4), (2, 1, 9)])
+def test_few_rows(cuda, G, Hkv, n, D):
+    """Rows times heads at and around 16 (products of 64 rows), alone, behind whole tiles, and cut over many CTAs; a
+    maximum that moves late."""
+    tile = 2 * (128 // G)
+    reqs = [(n, 700, 0, 0), (n, 64 * 3, n, 65), (n, n, 0, 0), (n, 5000, 0, 130), (tile + n, 400 + tile, 1, 0)]
+    c = make_case(reqs, G * Hkv, Hkv, D, seed=n + G)
+    out, lse, st = launch(cuda, c)
+    assert st == 0
+    check(c, out, lse)
+    out, lse, st = launch(cuda, c, scale=3.0 * D ** -0.5)
+    assert st == 0
+    check(c, out, lse, scale=3.0 * D ** -0.5)
