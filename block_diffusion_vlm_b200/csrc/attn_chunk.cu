@@ -51,7 +51,9 @@ namespace {
 constexpr int kAcThreads = 320;  // warp 0 loads and schedules, 1 issues MMAs, 2..5 and 6..9 softmax
 constexpr int kAcKeys = 64;      // slots per step: one page
 constexpr int kAcRing = 4;       // work descriptors in flight
-constexpr int kAcItemCost = 320; // fixed cost of an item, in slot units (prologue and epilogue: 4300 cycles, a slot of a tile 14.5)
+// Fixed cost of an item, in slots of a tile (prologue and epilogue take 4300
+// cycles, a slot 14.5; 256 to 512 measure alike).
+constexpr int kAcItemCost = 320;
 constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
