@@ -134,6 +134,7 @@ def _declare(L: ctypes.CDLL) -> None:
         "dvlm_chunk_attn_paged_workspace_size": (_sz, [_i] * 5),
         "dvlm_chunk_attn_paged": (_i, [_vp] * 10 + [_i] * 7 + [_ll, _f, _vp, _sz, _vp, _vp]),
         "dvlm_spec_verify_sample": (_i, [_vp] * 6 + [_i] * 4 + [_vp] * 6),
+        "dvlm_spec_verify_sample_rows": (_i, [_vp] * 6 + [_i] * 4 + [_vp] * 7),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -416,15 +417,22 @@ def chunk_attn_paged(q, out, k_pages, v_pages, block_table, kv_len, cu_rows, *, 
 
 
 def spec_verify_sample(target_p, draft_p, draft_ids, u_accept, u_sample, *, b, K, V, dtype, accept_len, out_ids,
-                       n_draft=None, cache_len=None, cache_len_out=None, status=None, stream=None) -> None:
-    """Verify drafts by rejection sampling with given random numbers (dvlm_spec_verify_sample)."""
+                       n_draft=None, cache_len=None, cache_len_out=None, cu_rows=None, status=None,
+                       stream=None) -> None:
+    """Verify drafts by rejection sampling with given random numbers (dvlm_spec_verify_sample).  cu_rows: the
+    plan's row offsets; requests without rows in the step are then left alone (dvlm_spec_verify_sample_rows)."""
     dev, i32, f32 = _device("dvlm_spec_verify_sample", target_p), _i32, _f32
     td = f32 if dtype == DVLM_FP32 else _bf16
     p = _take("dvlm_spec_verify_sample", dev, (target_p, td, b * (K + 1) * V), (draft_p, td, b * K * V),
               (draft_ids, i32, b * K), (n_draft, i32, b), (u_accept, f32, b * K), (u_sample, f32, b),
               (accept_len, i32, b), (out_ids, i32, b * (K + 1)), (cache_len, i32, b), (cache_len_out, i32, b),
-              (status, i32, 1))
-    _launch(lib().dvlm_spec_verify_sample, "dvlm_spec_verify_sample", dev, stream, *p[:6], b, K, V, dtype, *p[6:])
+              (cu_rows, i32, b + 1), (status, i32, 1))
+    if cu_rows is None:
+        _launch(lib().dvlm_spec_verify_sample, "dvlm_spec_verify_sample", dev, stream, *p[:6], b, K, V, dtype, *p[6:10],
+                p[11])
+    else:
+        _launch(lib().dvlm_spec_verify_sample_rows, "dvlm_spec_verify_sample_rows", dev, stream, *p[:6], b, K, V,
+                dtype, *p[6:])
 
 
 # ---------------------------------------------------------------- engine

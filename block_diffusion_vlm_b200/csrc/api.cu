@@ -541,21 +541,39 @@ dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void* k_pages,
   return cuda_status(launch_attn_chunk(mq, mk, mv, a, D, P, cs(stream)));
 }
 
+namespace {
+dvlm_status verify_sample(const SpecSampleArgs& a, dvlm_dtype dt, dvlm_stream stream) {
+  if (!a.target_p || !a.draft_ids || !a.u_accept || !a.u_sample || !a.accept_len || !a.out_ids)
+    return DVLM_ERR_INVALID_ARG;
+  if ((a.cache_len != nullptr) != (a.cache_len_out != nullptr)) return DVLM_ERR_INVALID_ARG;
+  if (dt != DVLM_BF16 && dt != DVLM_FP32) return DVLM_ERR_INVALID_ARG;
+  const uintptr_t es = dt == DVLM_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(a.target_p) % es || reinterpret_cast<uintptr_t>(a.draft_p) % es)
+    return DVLM_ERR_INVALID_ARG;
+  if (a.b < 1 || a.b > 65535 || a.K < 1 || a.K > 64 || a.V < 1 || a.V > (1 << 30)) return DVLM_ERR_SHAPE;
+  return cuda_status(launch_spec_sample(a, dt == DVLM_BF16, cs(stream)));
+}
+}  // namespace
+
 dvlm_status dvlm_spec_verify_sample(const void* target_p, const void* draft_p, const int32_t* draft_ids,
                                     const int32_t* n_draft, const float* u_accept, const float* u_sample, int b, int K,
                                     int V, dvlm_dtype dt, int32_t* accept_len, int32_t* out_ids,
                                     const int32_t* cache_len, int32_t* cache_len_out, int* dev_status,
                                     dvlm_stream stream) {
-  if (!target_p || !draft_ids || !u_accept || !u_sample || !accept_len || !out_ids) return DVLM_ERR_INVALID_ARG;
-  if ((cache_len != nullptr) != (cache_len_out != nullptr)) return DVLM_ERR_INVALID_ARG;
-  if (dt != DVLM_BF16 && dt != DVLM_FP32) return DVLM_ERR_INVALID_ARG;
-  const uintptr_t es = dt == DVLM_BF16 ? 2 : 4;
-  if (reinterpret_cast<uintptr_t>(target_p) % es || reinterpret_cast<uintptr_t>(draft_p) % es)
-    return DVLM_ERR_INVALID_ARG;
-  if (b < 1 || b > 65535 || K < 1 || K > 64 || V < 1 || V > (1 << 30)) return DVLM_ERR_SHAPE;
-  SpecSampleArgs a{target_p, draft_p, draft_ids, n_draft, u_accept, u_sample, b, K, V,
-                   accept_len, out_ids, cache_len, cache_len_out, dev_status};
-  return cuda_status(launch_spec_sample(a, dt == DVLM_BF16, cs(stream)));
+  return verify_sample(SpecSampleArgs{target_p, draft_p, draft_ids, n_draft, u_accept, u_sample, b, K, V, accept_len,
+                                      out_ids, cache_len, cache_len_out, nullptr, dev_status},
+                       dt, stream);
+}
+
+dvlm_status dvlm_spec_verify_sample_rows(const void* target_p, const void* draft_p, const int32_t* draft_ids,
+                                         const int32_t* n_draft, const float* u_accept, const float* u_sample, int b,
+                                         int K, int V, dvlm_dtype dt, int32_t* accept_len, int32_t* out_ids,
+                                         const int32_t* cache_len, int32_t* cache_len_out, const int32_t* cu_rows,
+                                         int* dev_status, dvlm_stream stream) {
+  if (!cu_rows) return DVLM_ERR_INVALID_ARG;
+  return verify_sample(SpecSampleArgs{target_p, draft_p, draft_ids, n_draft, u_accept, u_sample, b, K, V, accept_len,
+                                      out_ids, cache_len, cache_len_out, cu_rows, dev_status},
+                       dt, stream);
 }
 
 // ------------------------------------------------------------ FP8 weights

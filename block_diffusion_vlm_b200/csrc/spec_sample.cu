@@ -105,12 +105,30 @@ __global__ void __launch_bounds__(kSvThreads, 2) spec_sample_kernel(const SpecSa
   const T* tp = static_cast<const T*>(a.target_p) + static_cast<size_t>(seq) * (K + 1) * V;
   const T* dp = a.draft_p ? static_cast<const T*>(a.draft_p) + static_cast<size_t>(seq) * K * V : nullptr;
   const int32_t* ids = a.draft_ids + static_cast<size_t>(seq) * K;
+  // A sequence without rows in the step (waiting for pages, idle, finished,
+  // refused by the plan) has nothing to verify: its cache holds no drafts to
+  // cut off, and its probabilities are those of no row.
+  int most = K;
+  if (a.cu_rows) {
+    const long long rows = static_cast<long long>(a.cu_rows[seq + 1]) - a.cu_rows[seq];
+    if (rows <= 0) {
+      if (rank == 0) {
+        for (int j = threadIdx.x; j <= K; j += kSvThreads) a.out_ids[static_cast<size_t>(seq) * (K + 1) + j] = -1;
+        if (threadIdx.x == 0) {
+          a.accept_len[seq] = 0;
+          if (a.cache_len_out) a.cache_len_out[seq] = a.cache_len[seq];
+        }
+      }
+      return;  // (the whole cluster, before its first barrier)
+    }
+    most = static_cast<int>(min(rows, static_cast<long long>(K)));
+  }
   cluster_arrive();  // every CTA of the cluster runs before any sends into it (the wait sits before the sends)
 
   int nd = a.n_draft ? a.n_draft[seq] : K;
-  if (nd < 0 || nd > K) {
+  if (nd < 0 || nd > most) {
     if (threadIdx.x == 0) record_error(a.status, DVLM_ERR_BOUNDS);
-    nd = nd < 0 ? 0 : K;
+    nd = nd < 0 ? 0 : most;
   }
   // every CTA of the cluster takes the K decisions for itself
   if (warp == 0) {

@@ -18,6 +18,7 @@ struct SpecSampleArgs {
   int32_t* out_ids;           // [b][K + 1]
   const int32_t* cache_len;   // [b] (NULL with cache_len_out)
   int32_t* cache_len_out;
+  const int32_t* cu_rows;     // [b + 1] row offsets of the step that ran, or NULL: every sequence ran
   int* status;
 };
 cudaError_t launch_spec_sample(const SpecSampleArgs& a, bool is_bf16, cudaStream_t s);

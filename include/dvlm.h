@@ -275,7 +275,7 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * tables and a slot map (dvlm_page_plan), the projected rows become rotated
  * queries and cached keys and values (dvlm_mrope_append_paged), every request's
  * rows attend to its pages (dvlm_chunk_attn_paged), and drafted tokens are
- * verified against the target's probabilities (dvlm_spec_verify_sample).  The
+ * verified against the target's probabilities (dvlm_spec_verify_sample_rows).  The
  * page stores, block tables and lengths are those of dvlm_block_attn_paged
  * [Fast-dVLM technical overview (ocdem.com), section 2.3.2: paged KV cache
  * management].  The rows of all requests of a step are packed one request
@@ -416,12 +416,25 @@ DVLM_API dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void*
  * from the target row itself; if that is 0 too, token 0 and DVLM_ERR_BOUNDS.
  * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS), as is an n_draft
  * outside 0..K (cut to it).  1 <= K <= 64, b <= 65535, V <= 2^30.  Sums and
- * decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace. */
+ * decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace.
+ *
+ * Behind dvlm_page_plan use the _rows form: it takes the plan's cu_rows [b + 1]
+ * (device int32), for only the device knows which requests got their rows.  A
+ * request without rows (waiting, idle, finished, refused) has nothing to
+ * verify: accept_len 0, every out_ids -1, its cache length as it is.  An
+ * n_draft (or K, with n_draft NULL) above a request's rows is cut to them
+ * (DVLM_ERR_BOUNDS).  Without cu_rows every sequence counts as having run. */
 DVLM_API dvlm_status dvlm_spec_verify_sample(const void* target_p, const void* draft_p, const int32_t* draft_ids,
                                             const int32_t* n_draft, const float* u_accept, const float* u_sample,
                                             int b, int K, int V, dvlm_dtype dt, int32_t* accept_len,
                                             int32_t* out_ids, const int32_t* cache_len, int32_t* cache_len_out,
                                             int* dev_status, dvlm_stream stream);
+DVLM_API dvlm_status dvlm_spec_verify_sample_rows(const void* target_p, const void* draft_p,
+                                                 const int32_t* draft_ids, const int32_t* n_draft,
+                                                 const float* u_accept, const float* u_sample, int b, int K, int V,
+                                                 dvlm_dtype dt, int32_t* accept_len, int32_t* out_ids,
+                                                 const int32_t* cache_len, int32_t* cache_len_out,
+                                                 const int32_t* cu_rows, int* dev_status, dvlm_stream stream);
 
 /* ------------------------------------------------------------------------
  * Decoder model and decode engine.

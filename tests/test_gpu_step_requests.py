@@ -1,0 +1,113 @@
+"""The batched paged step around requests that take no rows, and at the edges
+of its page numbers, drafts and values, against the plain 64-bit definitions
+(step_reference.py).  Integers are equal; attention is held to the bound of
+test_gpu_chunk_attn.py."""
+import numpy as np
+import pytest
+import torch
+
+import block_diffusion_vlm_b200 as dv
+import step_reference as ref
+from gpu_util import assert_ok, status
+from test_gpu_step_run import Server, host
+
+pytestmark = pytest.mark.gpu
+OVERFLOW, BOUNDS = 4, 8
+
+
+def i32(v, dev):
+    return torch.tensor(np.asarray(v, dtype=np.int32), device=dev)
+
+
+# ------------------------------------------------- requests without rows in a step
+class StepServer(Server):
+    """A server whose verification knows which requests got rows."""
+
+    def step(self, verify, n_draft=True):
+        super().step(False)                     # (the cache then counts every new row)
+        if verify:
+            dv.spec_verify_sample(self.p, None, self.ids, self.u, self.us, b=self.n, K=self.K, V=self.V,
+                                  dtype=dv.DVLM_FP32, accept_len=self.acc, out_ids=self.tok,
+                                  n_draft=self.nd if n_draft else None, cache_len=self.kv, cache_len_out=self.cache,
+                                  cu_rows=self.cu, status=self.st)
+
+
+def check_verified(s, n_draft):
+    """Tokens, accepted lengths and cut caches of a step; returns the requests that ran."""
+    cu, kv, acc, tok, cut = host(s.cu), host(s.kv), host(s.acc), host(s.tok), host(s.cache)
+    ran = []
+    for b in range(s.n):
+        rows = int(cu[b + 1] - cu[b])
+        if rows == 0:
+            assert (acc[b], tok[b].tolist(), cut[b]) == (0, [-1] * (s.K + 1), kv[b]), b
+            continue
+        ran.append(b)
+        nd = min(n_draft[b], rows)
+        k, ids, bad = ref.verify(host(s.p[b]).astype(np.float64), None, host(s.ids[b]).tolist(),
+                                 host(s.u[b]).astype(np.float64), float(s.us[b]), nd)
+        assert (acc[b], tok[b].tolist(), cut[b]) == (k, ids, kv[b] - (nd - k)) and not bad, b
+    return ran
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_requests_without_rows_keep_their_caches(cuda, graph):
+    """Waiting, idle, finished and refused requests beside drafted ones: no token, no cut, no matter what n_draft says;
+    the waiting one goes on with its whole cache once another's pages come back."""
+    s = StepServer(cuda, n=6, max_pages=3, n_pages=10, max_rows=460)
+    put = lambda t, v: t.copy_(i32(v, cuda))
+    put(s.new, [60, 50, 20, 192, 63, 64])        # 1 + 1 + 1 + 3 + 1 + 1 pages of 10
+    s.fill()
+    s.step(False)
+    assert_ok(s.st)
+    if graph:
+        s.nd.fill_(6)
+        s.new.zero_()
+        s.step(True)                             # (warm-up: nothing runs, nothing changes)
+        assert_ok(s.st)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.step(True)
+
+    def step(new, n_draft, st):
+        put(s.new, new)
+        put(s.nd, n_draft)
+        s.fill()
+        s.st.zero_()
+        before, table, held = host(s.cache), host(s.table), host(s.held)
+        stack = host(s.free)[:int(s.count)].tolist()
+        g.replay() if graph else s.step(True)
+        torch.cuda.synchronize()
+        assert int(s.st) in st
+        want = ref.page_plan(before, new, table, stack, s.max_pages, s.n_pages, s.max_rows, held)
+        for got, w in zip((s.kv, s.cu, s.slots, s.table), want):
+            np.testing.assert_array_equal(host(got), w)
+        return check_verified(s, n_draft)
+
+    # two pages are left: the first three need one between them (60 + 6), then 3 is refused (192 + 1 slots), 4 takes
+    # the last page and 5 (64 + 6) waits
+    ran = step([6, 6, 0, 1, 6, 6], [6, 6, 6, 6, 6, 6], (OVERFLOW, BOUNDS))
+    assert ran == [0, 1, 4]
+    assert host(s.cache)[[2, 3, 5]].tolist() == [20, 192, 64] and int(s.count) == 0
+    # 3 finishes (its three pages come back), 5 goes on with all of its cache; one row holds no second draft
+    ran = step([0, 0, 1, -1, 0, 6], [6, 6, 0, 6, 6, 6], (0,))
+    assert ran == [2, 5] and host(s.kv)[[3, 5]].tolist() == [0, 70] and host(s.cache)[3] == 0
+    # more drafts than rows: cut to the rows, and said so
+    ran = step([0, 2, 0, 0, 0, 0], [6, 6, 6, 6, 6, 6], (BOUNDS,))
+    assert ran == [1]
+
+
+def test_verify_without_draft_counts(cuda):
+    """n_draft NULL means K for the sequences that ran; rows that descend count as none."""
+    s = StepServer(cuda, n=4, max_pages=2, n_pages=8, max_rows=64)
+    s.fill()
+    s.kv.copy_(i32([30, 40, 50, 60], cuda))
+    for cu, st in (([0, 6, 6, 13, 20], 0), ([0, 6, 4, 13, 16], BOUNDS)):
+        s.cu.copy_(i32(cu, cuda))
+        s.st.zero_()
+        dv.spec_verify_sample(s.p, None, s.ids, s.u, s.us, b=4, K=6, V=s.V, dtype=dv.DVLM_FP32, accept_len=s.acc,
+                              out_ids=s.tok, cache_len=s.kv, cache_len_out=s.cache, cu_rows=s.cu, status=s.st)
+        torch.cuda.synchronize()
+        assert int(s.st) == st
+        got = host(s.cu)
+        s.cu.copy_(torch.cat([s.cu[:1], s.cu[:1] + torch.cumsum((s.cu[1:] - s.cu[:-1]).clamp(min=0), 0)]))
+        assert check_verified(s, [6] * 4) == [b for b in range(4) if got[b + 1] > got[b]]
