@@ -223,7 +223,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
         const int slot = s_cache[b] + (i + e - s_row[b]), p = slot >> 6, held = s_held[b];
         if (p != last) {
           page = p < held ? a.block_table[static_cast<size_t>(b) * a.max_pages + p] : taken(s_need[b] + p - held);
-          page = max(-kPlanNoPage, min(page, kPlanNoPage));  // (a wild number's slots must not wrap into the store)
+          // a wild number's slots must not wrap into the store, and -1's must not
+          // reach slot -1, which means padding
+          page = page == -1 ? -2 : max(-kPlanNoPage, min(page, kPlanNoPage));
           last = p;
         }
         v[e] = page * 64 + (slot & 63);

@@ -306,7 +306,8 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
  * numbers are passed on as they are (in slot_map cut to +- (2^25 - 1), past any
- * store).  All pointers device int32.  n_batch <=
+ * store, and -1 taken for -2): a row on a number that is no page of the store
+ * never has slot -1, so that dvlm_mrope_append_paged reports it.  All pointers device int32.  n_batch <=
  * 4096, n_pages and max_pages < 2^25, n_batch * max_pages < 2^31, max_rows <=
  * 2^30.  Errors: INVALID_ARG, SHAPE.  One
  * launch, no workspace. */

@@ -111,3 +111,50 @@ def test_verify_without_draft_counts(cuda):
         got = host(s.cu)
         s.cu.copy_(torch.cat([s.cu[:1], s.cu[:1] + torch.cumsum((s.cu[1:] - s.cu[:-1]).clamp(min=0), 0)]))
         assert check_verified(s, [6] * 4) == [b for b in range(4) if got[b + 1] > got[b]]
+
+
+# ----------------------------------------------------------------- page numbers
+def plan_of(cuda, cache, new, table, stack, n_pages, max_rows):
+    n, max_pages = np.shape(table)
+    free = np.zeros(n_pages, dtype=np.int32)
+    free[:len(stack)] = stack
+    t = i32(table, cuda)
+    kv, cu, slots, count, st = i32([0] * n, cuda), i32([0] * (n + 1), cuda), i32([0] * max_rows, cuda), \
+        i32([len(stack)], cuda), status(cuda)
+    dv.page_plan(i32(cache, cuda), i32(new, cuda), t, i32(free, cuda), count, n_batch=n, max_pages=max_pages,
+                 n_pages=n_pages, max_rows=max_rows, kv_len=kv, cu_rows=cu, slot_map=slots, free_count_out=count,
+                 status=st)
+    assert_ok(st)
+    return slots, t
+
+
+def append_status(cuda, slots, rows, n_pages):
+    """Status of an append of `rows` rows of ones; the rows of q that were written."""
+    D = 64
+    bf = dict(dtype=torch.bfloat16, device=cuda)
+    q, st = torch.zeros(rows, 2, D, **bf), status(cuda)
+    dv.mrope_append_paged(torch.ones(rows, 4 * D, **bf), i32(np.zeros((1, rows)), cuda), slots, q,
+                          torch.zeros(n_pages, 1, 64, D, **bf), torch.zeros(n_pages, 1, D, 64, **bf), n_rows=rows,
+                          Hq=2, Hkv=1, D=D, n_pages=n_pages, sections=(32,), rope_base=1e4, status=st)
+    torch.cuda.synchronize()
+    return int(st), (q != 0).all(dim=(1, 2)).cpu().tolist()
+
+
+@pytest.mark.parametrize("wild", [-1, -2, -3, -2 ** 25, 4, 2 ** 25])
+def test_no_live_row_looks_like_padding(cuda, wild):
+    """A table entry or a stack entry that is no page (-1: the usual filler) gives slots that the append reports, the
+    last of the page too (slot -1 is padding: skipped without a word)."""
+    slots, _ = plan_of(cuda, [0], [64], [[-7]], [wild], 4, 66)       # off the stack
+    got = host(slots)
+    assert got[64:].tolist() == [-1, -1] and ((got[:64] >= 4 * 64) | (got[:64] < -1)).all()
+    assert (got[:64].astype(np.int64) % 64 == np.arange(64)).all()
+    for at in (0, 40, 63):                                           # a cached page, one row alone
+        slots, table = plan_of(cuda, [at], [1], [[wild if at else -7]], [] if at else [wild], 4, 1)
+        assert host(table).tolist() == [[wild]]                      # the table keeps what it was given
+        st, written = append_status(cuda, slots, 1, 4)
+        assert st == BOUNDS and written == [False], at
+    # the next request's rows are right all the same
+    slots, _ = plan_of(cuda, [63, 63], [1, 1], [[wild], [2]], [], 4, 3)
+    assert host(slots)[1:].tolist() == [2 * 64 + 63, -1]
+    st, written = append_status(cuda, slots, 3, 4)
+    assert st == BOUNDS and written == [False, True, False]
