@@ -755,8 +755,10 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         tmem_ld32_nowait(tP, s0);
         tmem_ld32_nowait(tP + 32, s1);
         // V of slots outside hidden .. kv - 1 may hold anything (stale pages):
-        // 0 there, for 0 * NaN is not 0
-        if (key0 + kAcKeys > k.kv || key0 < k.hid) {
+        // 0 there, for 0 * NaN is not 0.  A pair's page is cleared by the first
+        // tile's warps alone: both tiles' P V are issued, by one thread, behind
+        // the first tile's P, so none reads the page while it is written.
+        if ((solo || w == 0) && (key0 + kAcKeys > k.kv || key0 < k.hid)) {
           const int vp = pos + min(lag, k.nc) + c + min(c, max(0, k.nc - lag));
           if (!warp_wait(&kv_full[vp % NS], (vp / NS) & 1)) {
             ok = false;

@@ -9,6 +9,7 @@ import torch
 import block_diffusion_vlm_b200 as dv
 import step_reference as ref
 from gpu_util import assert_ok, status
+from test_gpu_chunk_attn import check, launch, make_case
 from test_gpu_step_run import Server, host
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +159,20 @@ def test_no_live_row_looks_like_padding(cuda, wild):
     assert host(slots)[1:].tolist() == [2 * 64 + 63, -1]
     st, written = append_status(cuda, slots, 3, 4)
     assert st == BOUNDS and written == [False, True, False]
+
+
+# ------------------------------------------------------- slots that no row may see
+@pytest.mark.parametrize("D", [64, 128])
+def test_stale_values_beside_two_tiles(cuda, D):
+    """Pairs of row tiles whose first or last page is partly outside the cache, with NaN there (one tile's warps clear
+    V for both): hidden prefixes and ends at every kind of place, rows that see only such a page, again and again."""
+    reqs = [(256, 256 + kv, noisy, hid) for kv, noisy, hid in ((1, 0, 0), (63, 0, 63), (7, 256, 5), (130, 40, 129),
+                                                               (0, 0, 200), (300, 0, 1), (65, 256, 320), (64, 0, 64))]
+    c = make_case(reqs, 8, 1, D, seed=21)
+    out0, lse0, st = launch(cuda, c)
+    assert st == 0
+    check(c, out0, lse0, rows_of={0, 1, 3, 6})
+    assert np.isfinite(out0).all()
+    for _ in range(20):
+        out, lse, st = launch(cuda, c)
+        assert st == 0 and np.array_equal(out, out0) and np.array_equal(lse, lse0)
