@@ -826,7 +826,8 @@ __global__ void __launch_bounds__(kAcThreads, 1)
         const float a0 = w == 0 ? a_own : a_oth, a1 = w == 0 ? a_oth : a_own;
         const float lt = l * a_own + o2.y * a_oth;
         const bool h0 = k.nc > 0, h1 = k.nc > 1;
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const float nan = lt == lt ? 0.f : lt;  // scores that are no numbers, which the maxima pass over
         const float f0 = k.slot < 0 ? a0 * inv : a0, f1 = k.slot < 0 ? a1 * inv : a1;
         constexpr int HD = D / 2;
 #pragma unroll 1
@@ -837,18 +838,18 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           tmem_ld16(tl + kAcColO + D + col, y);
 #pragma unroll
           for (int j = 0; j < 16; ++j)  // an accumulator that no page reached holds anything
-            x[j] = (h0 && a0 > 0.f ? x[j] * f0 : 0.f) + (h1 && a1 > 0.f ? y[j] * f1 : 0.f);
+            x[j] = (h0 && a0 > 0.f ? x[j] * f0 : nan) + (h1 && a1 > 0.f ? y[j] * f1 : nan);
           store_cols(k, tok, valid, 0, col, x);
         }
         if (w == 0 && valid) {
           if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + row] = make_float2(mm, lt);
           else if (a.lse)
             a.lse[static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh] =
-                lt > 0.f ? (mm * sl2 + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                lt == 0.f ? -INFINITY : (mm * sl2 + log2f(lt)) * 0.69314718055994531f;
         }
         if (!meet()) break;  // both accumulators and sML read
       } else {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // (NaN stays NaN)
         const float f = k.slot < 0 ? inv : 1.f;
 #pragma unroll 1
         for (int cc = 0; live && cc < D; cc += 64) {
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           for (int h = 0; h < 4; ++h) {
             float x[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = k.nc > 0 && l > 0.f ? __uint_as_float(u[h >> 1][(h & 1) * 16 + j]) * f : 0.f;
+            for (int j = 0; j < 16; ++j) x[j] = k.nc > 0 && l != 0.f ? __uint_as_float(u[h >> 1][(h & 1) * 16 + j]) * f : 0.f;
             store_cols(k, tok, valid, w, cc + h * 16, x);
           }
         }
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(kAcThreads, 1)
           if (k.slot >= 0) ws.ml[(cta * 2 + k.slot) * 256 + w * 128 + row] = make_float2(m, l);
           else if (a.lse)
             a.lse[static_cast<size_t>(k.row0 + tok) * a.Hq + k.g * G + rh] =
-                l > 0.f ? (m * sl2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                l == 0.f ? -INFINITY : (m * sl2 + log2f(l)) * 0.69314718055994531f;
         }
         tc_fence_before();
       }
@@ -974,7 +975,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attn_chunk_merge_kernel(const C
       }
       m = mn;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const size_t o_at = static_cast<size_t>(row0 + tok) * a.Hq + g * G + rh;
     uint32_t pk[F / 2];
 #pragma unroll
@@ -982,7 +983,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attn_chunk_merge_kernel(const C
     uint2* dst = reinterpret_cast<uint2*>(a.out + o_at * D + part * F);
 #pragma unroll
     for (int q = 0; q < F / 4; ++q) dst[q] = make_uint2(pk[2 * q], pk[2 * q + 1]);
-    if (a.lse && part == 0) a.lse[o_at] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse && part == 0) a.lse[o_at] = l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f;
   }
 }
 

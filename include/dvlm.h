@@ -374,7 +374,8 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
  * (n_pages * Hkv * max(D, 64)) stay below 2^31; n_batch <= 2^24, n_rows <= 2^30.
  * scale > 0 (scale * log2(e) a finite fp32).  Hidden slots and
  * those at or beyond kv_len[b] may hold anything, NaN included; the slots
- * between must be finite.  Scores, softmax and sums in fp32, P in bf16.  The
+ * between must be finite.  A query that holds a NaN, or an infinity that meets
+ * keys of both signs, gives NaN in its row of out and lse, and in no other.  Scores, softmax and sums in fp32, P in bf16.  The
  * result of a row depends on the other requests of the call only in the
  * order of its fp32 sums; the same call gives the same bits.  A request whose
  * cu_rows descend or leave 0 .. n_rows, whose kv_len is outside 0 .. 64

@@ -176,3 +176,30 @@ def test_stale_values_beside_two_tiles(cuda, D):
     for _ in range(20):
         out, lse, st = launch(cuda, c)
         assert st == 0 and np.array_equal(out, out0) and np.array_equal(lse, lse0)
+
+
+# ------------------------------------------------------ values that are no numbers
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 128), (14, 2, 64), (8, 8, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_no_numbers(cuda, Hq, Hkv, D, bad):
+    """A query with a NaN, or with an infinity (scores of both signs: inf - inf), gives NaN and not 0, which stands for
+    a row that sees nothing; the other rows and heads keep their bits.  Whole tiles, pairs of tiles, single tokens, and
+    items cut over many CTAs."""
+    reqs = [(1, 300, 0, 0), (16, 130, 16, 0), (40, 40, 0, 0), (300, 900, 0, 0), (1, 9000, 0, 0), (16, 7000, 16, 0),
+            (4, 70, 0, 70)]
+    c = make_case(reqs, Hq, Hkv, D, seed=11)
+    out0, lse0, st = launch(cuda, c)
+    assert st == 0
+    rows = [int(c["cu"][b]) + t for b, t in ((0, 0), (1, 7), (2, 39), (3, 0), (3, 171), (3, 299), (4, 0), (5, 3))]
+    head = Hq - 1
+    for r in rows:
+        c["q"][r, head * D + 5] = bad
+    hidden = int(c["cu"][6])                                          # a row that sees nothing is 0 whatever it holds
+    c["q"][hidden, head * D + 5] = bad
+    out, lse, st = launch(cuda, c)
+    assert st == 0
+    assert np.isnan(out[rows, head]).all() and np.isnan(lse[rows, head]).all()
+    assert (out[hidden:hidden + 4] == 0).all() and np.isneginf(lse[hidden:hidden + 4]).all()
+    keep = np.ones(out.shape[:2], dtype=bool)
+    keep[rows, head] = False
+    assert np.array_equal(out[keep], out0[keep]) and np.array_equal(lse[keep], lse0[keep])
