@@ -135,22 +135,22 @@ __global__ void __launch_bounds__(kSvThreads, 2) spec_sample_kernel(const SpecSa
     int k = nd;
     for (int j0 = 0; j0 < nd; j0 += 32) {
       const int j = j0 + lane;
-      bool ok = true;
+      bool ok = true, known = true;
       if (j < nd) {
         const int x = ids[j];
-        ok = x >= 0 && x < V;
+        ok = known = x >= 0 && x < V;
         if (ok) {
           const size_t at = static_cast<size_t>(j) * V + x;
           const float p = as_f(tp[at]), q = dp ? as_f(dp[at]) : 1.f;
           const double u = a.u_accept[static_cast<size_t>(seq) * K + j];
           ok = u * q < p && fmaxf(fabsf(p), fabsf(q)) < INFINITY;
-        } else if (rank == 0) {
-          record_error(a.status, DVLM_ERR_BOUNDS);
         }
       }
       const unsigned rej = __ballot_sync(0xffffffffu, !ok);
       if (rej) {
         k = j0 + __ffs(rej) - 1;
+        // (drafts behind the first refused one are not looked at)
+        if (j == k && !known && rank == 0) record_error(a.status, DVLM_ERR_BOUNDS);
         break;
       }
     }

@@ -416,8 +416,8 @@ DVLM_API dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void*
  * a draft.  u_sample outside
  * [0, 1) counts as the nearest value inside.  If r is 0 everywhere the draw is
  * from the target row itself; if that is 0 too, token 0 and DVLM_ERR_BOUNDS.
- * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS), as is an n_draft
- * outside 0..K (cut to it).  1 <= K <= 64, b <= 65535, V <= 2^30.  Sums and
+ * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS; behind a refused draft
+ * none is looked at), as is an n_draft outside 0..K (cut to it).  1 <= K <= 64, b <= 65535, V <= 2^30.  Sums and
  * decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace.
  *
  * Behind dvlm_page_plan use the _rows form: it takes the plan's cu_rows [b + 1]

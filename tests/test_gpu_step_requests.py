@@ -10,6 +10,7 @@ import block_diffusion_vlm_b200 as dv
 import step_reference as ref
 from gpu_util import assert_ok, status
 from test_gpu_chunk_attn import check, launch, make_case
+from test_gpu_step import run_verify
 from test_gpu_step_run import Server, host
 
 pytestmark = pytest.mark.gpu
@@ -203,3 +204,29 @@ def test_queries_that_are_no_numbers(cuda, Hq, Hkv, D, bad):
     keep = np.ones(out.shape[:2], dtype=bool)
     keep[rows, head] = False
     assert np.array_equal(out[keep], out0[keep]) and np.array_equal(lse[keep], lse0[keep])
+
+
+# ------------------------------------------------------------------------ drafts
+@pytest.mark.parametrize("K", [3, 31, 33, 64])
+def test_drafts_behind_a_refused_one_are_not_looked_at(cuda, K):
+    """Ids outside the vocabulary are reported where the verification gets to them, and not behind a refused draft."""
+    V, b = 96, 4
+    p = torch.full((b, K + 1, V), 1.0 / V)
+    ids, u = np.full((b, K), 7), np.zeros((b, K), dtype=np.float32)
+    u[0, 0], u[1, K - 2] = 1.0, 1.0                     # sequences 0 and 1 refuse a draft; 2 and 3 take every one
+    p[:2, :, 7] = 0.0
+    p[1, :K - 2, 7] = 1.0 / V
+    for bad in ([(0, 1)], [(0, K - 1), (1, K - 1)], [(0, j) for j in range(1, K)]):
+        x = ids.copy()
+        for i, j in bad:
+            x[i, j] = -1 if j % 2 else V
+        for q in (None, torch.full((b, K, V), 1.0 / V)):
+            acc, out, _, st = run_verify(cuda, p, q, x, u, np.full(b, 0.25))
+            assert st == 0 and acc.tolist() == [0, K - 2, K, K], bad
+    for i, j in ((2, K - 1), (3, 0), (1, K - 2), (0, 0)):               # reached: reported
+        x = ids.copy()
+        x[i, j] = V + 3
+        acc, out, _, st = run_verify(cuda, p, None, x, u, np.full(b, 0.25))
+        assert st == BOUNDS and acc[i] == j
+        k, want, bad = ref.verify(p[i].double().numpy(), None, x[i].tolist(), u[i].astype(np.float64), 0.25, K)
+        assert bad and out[i].tolist() == want
