@@ -362,7 +362,7 @@ namespace {
 // Head groups per row: one where the rows alone fill the GPU's warps, else as
 // many as give each SM a few warps of work, down to one head.
 int head_groups(int n_rows, int heads) {
-  const int want = 148 * 16 / n_rows;
+  const int want = device_sm_count() * 16 / n_rows;
   return want < 1 ? 1 : (want > heads ? heads : want);
 }
 // Blocks for n_units warps of work, at most twice what the SMs hold at once
