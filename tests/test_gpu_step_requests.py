@@ -230,3 +230,69 @@ def test_drafts_behind_a_refused_one_are_not_looked_at(cuda, K):
         assert st == BOUNDS and acc[i] == j
         k, want, bad = ref.verify(p[i].double().numpy(), None, x[i].tolist(), u[i].astype(np.float64), 0.25, K)
         assert bad and out[i].tolist() == want
+
+
+def test_a_request_alone_and_in_a_batch(cuda):
+    """The other requests move the cuts of a request's work and with them the reference maxima against which P is
+    rounded: alone and in any batch a row keeps to the bound around its exact value, so the two are within twice that
+    bound of each other (they are not the same bits)."""
+    Hq, Hkv, D = 16, 2, 128
+    mine = [(16, 900, 16, 0), (1, 5000, 0, 0), (200, 700, 0, 100)]
+    other = [(1, 3000, 0, 0), (300, 2000, 0, 0), (16, 64, 16, 0), (33, 1500, 0, 0)]
+    c = make_case(mine + other, Hq, Hkv, D, seed=12)
+    outs = []
+    for take in ([0], [1], [2], [0, 1, 2], list(range(7))):
+        part = dict(c, reqs=[c["reqs"][b] for b in take], table=c["table"][take])
+        part["q"] = torch.cat([c["q"][c["cu"][b]:c["cu"][b + 1]] for b in take] + [c["q"][-3:]])
+        part["cu"] = np.concatenate([[0], np.cumsum([r[0] for r in part["reqs"]])])
+        part["rows"] = int(part["cu"][-1])
+        out, lse, st = launch(cuda, part)
+        assert st == 0
+        check(part, out, lse)                              # each within the bound of the exact value
+        outs.append({b: out[part["cu"][i]:part["cu"][i + 1]] for i, b in enumerate(take)})
+    kp, vp = np.nan_to_num(c["kp"].double().numpy()), np.nan_to_num(c["vp"].double().numpy())
+    for b in range(3):
+        n, kv, noisy, hid = c["reqs"][b]
+        q = c["q"][c["cu"][b]:c["cu"][b + 1]].double().numpy().reshape(n, Hq, D)
+        args = (c["table"][b].tolist(), kv, noisy, hid, D ** -0.5)
+        want, _ = ref.chunk_attention(q, kp, vp, *args)
+        mag, _ = ref.chunk_attention(q, kp, np.abs(vp), *args)
+        one = mag * (2.0 ** -8 + 2.0 ** -12) + (np.abs(want) + mag * 2.0 ** -8) * 2.0 ** -8
+        for o in outs[3:]:
+            assert (np.abs(o[b] - outs[b][b]) <= 2 * one).all()
+
+
+# --------------------------------------------------------------- batches together
+def test_two_batches_at_once_all_steps(cuda):
+    """Two batches, each on its own stream with its own workspace, through steps that all fit: the same lengths,
+    tokens, attention, log-sum-exp and page stores as one by one, and no error."""
+    def make():
+        out = []
+        for seed, new in ((1, [100, 1, 17]), (2, [3, 90, 64])):
+            s = StepServer(cuda, n=3, max_pages=12, n_pages=30, max_rows=300, seed=seed)
+            s.new.copy_(i32(new, cuda))
+            s.nd.copy_(i32([3, 1, 0], cuda))
+            s.fill()
+            out.append(s)
+        return out
+
+    alone, both = make(), make()
+    torch.cuda.synchronize()
+    for s in alone:
+        for _ in range(6):
+            s.step(True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(6):
+        for s, stream in zip(both, streams):
+            with torch.cuda.stream(stream):
+                s.step(True)
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        assert_ok(x.st)
+        assert_ok(y.st)
+        assert torch.equal(x.cu[1:] - x.cu[:-1], x.new)               # every request had its rows in the last step too
+        for k in ("kv", "cache", "held", "table", "slots", "free", "count", "acc", "tok", "lse"):
+            assert torch.equal(getattr(x, k), getattr(y, k)), k
+        for k in ("q", "out", "kp", "vp"):
+            assert torch.equal(getattr(x, k).view(torch.int16), getattr(y, k).view(torch.int16)), k
