@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const PagePl
     for (int i = 0; i < kPlanPer; ++i) {
       const int b = tid * per + i;
       if (i >= per || b >= n) continue;
-      a.kv_len[b] = live[i] ? cache[i] + (fits[i] ? want[i] : 0) : 0;
+      // (in place, the length of a request that takes no part is not lost: its pages can still be given back)
+      if (part[i] || a.kv_len != a.cache_len) a.kv_len[b] = live[i] ? cache[i] + (fits[i] ? want[i] : 0) : 0;
       a.cu_rows[b] = s_row[b];
       if (a.held_len && part[i]) a.held_len[b] = live[i] ? max(a.held_len[b], cache[i] + (fits[i] ? want[i] : 0)) : 0;
     }

@@ -302,8 +302,8 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * kv_len (0 for a finished request).  kv_len may be cache_len and
  * free_count_out may be free_count; no other arrays may overlap.  A request whose cached
  * length is outside 0 .. 64 max_pages, whose held length is above that, whose new length is below -1, or whose sum is
- * past 64 max_pages takes no part (kv_len: 0 in the first two cases, its
- * cached length in the last) and sets DVLM_ERR_BOUNDS, as does a free_count
+ * past 64 max_pages takes no part (kv_len: its cached length in the last case; 0
+ * in the others, or left as it is where kv_len is cache_len) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
  * numbers are passed on as they are (in slot_map cut to +- (2^25 - 1), past any
  * store, and -1 taken for -2): a row on a number that is no page of the store

@@ -115,6 +115,34 @@ def test_verify_without_draft_counts(cuda):
         assert check_verified(s, [6] * 4) == [b for b in range(4) if got[b + 1] > got[b]]
 
 
+@pytest.mark.parametrize("with_held", [False, True])
+@pytest.mark.parametrize("bad", [-2, -2 ** 31])
+def test_a_bad_new_length_loses_no_cache_in_place(cuda, with_held, bad):
+    """kv_len in cache_len's place: a request refused for its new length keeps its length, and gives all of its pages
+    back when it finishes; beside it the others go on."""
+    n, max_pages, n_pages = 3, 4, 12
+    table = np.full((n, max_pages), -1, dtype=np.int32)
+    table[0, :2], table[1, :3] = [3, 5], [7, 8, 9]
+    free = np.zeros(n_pages, dtype=np.int32)
+    free[:7] = [0, 1, 2, 4, 6, 10, 11]
+    t, f, count, st = i32(table, cuda), i32(free, cuda), i32([7], cuda), status(cuda)
+    cache, held = i32([100, 150, 0], cuda), i32([100, 190, 0], cuda) if with_held else None
+    cu, slots = i32([0] * (n + 1), cuda), i32([0] * 70, cuda)
+
+    def plan(new):
+        st.zero_()
+        dv.page_plan(cache, i32(new, cuda), t, f, count, n_batch=n, max_pages=max_pages, n_pages=n_pages, max_rows=70,
+                     kv_len=cache, cu_rows=cu, slot_map=slots, free_count_out=count, held_len=held, status=st)
+        torch.cuda.synchronize()
+        return int(st)
+
+    assert plan([10, bad, 5]) == BOUNDS
+    assert host(cache).tolist() == [110, 150, 5] and host(cu).tolist() == [0, 10, 10, 15] and int(count) == 6
+    assert plan([0, -1, 0]) == 0
+    assert host(cache).tolist() == [110, 0, 5] and int(count) == 9
+    assert sorted(host(f)[:9].tolist() + [3, 5, int(host(t)[2, 0])]) == list(range(12))
+
+
 # ----------------------------------------------------------------- page numbers
 def plan_of(cuda, cache, new, table, stack, n_pages, max_rows):
     n, max_pages = np.shape(table)
