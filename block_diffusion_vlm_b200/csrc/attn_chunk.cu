@@ -25,9 +25,11 @@
 //
 // Bound and measure: a page of a pair item takes about 2100 cycles, of which
 // the exponentials of its 256 x 64 scores hold their unit for 1024 and the
-// products the tensor pipe for 1260; chunks of rows run into the 1000 W power
-// cap (1.74 of 1.965 GHz).  4096 rows over 12288 slots, 16/2 heads of 128: 332
-// us, 1.04 PFLOP/s.  Steps of two pages with one score buffer: 340 to 366 us
+// products the tensor pipe for 1050 (both 50% by the profiler's counters; 2 x
+// 256 x 64 x 128 multiply-adds at the pipe's 4096 a cycle are 1024); chunks of
+// rows run into the 1000 W power cap (1.74 of 1.965 GHz).  4096 rows over 12288
+// slots, 16/2 heads of 128: 332 us (1.04 PFLOP/s) in short runs, 347 us back to
+// back and 355 us after a second of nothing else (0.97 PFLOP/s).  Steps of two pages with one score buffer: 340 to 366 us
 // (the scores' latency stands between two steps); four warpgroups with the
 // keys of a page halved between two: 352 us, and with a second issuing thread
 // 350 us at lower clocks; a quarter or half of the exponentials as a
@@ -54,7 +56,10 @@ constexpr int kAcRing = 4;       // work descriptors in flight
 // Fixed cost of an item, in slots of a tile (prologue and epilogue take 4300
 // cycles, a slot 14.5; 256 to 512 measure alike).
 constexpr int kAcItemCost = 320;
-constexpr int kAcMinPart = 256;  // least cost worth a CTA of its own
+// Least cost worth a CTA of its own.  16 rows over 1360 slots 12.9 us, one
+// token over 500 slots 11.7, over 4000 14.1; with 128: 12.3, 10.5 and 15.1;
+// with 512: 15.8, 13.7 and 15.3; with 1024: 20.6, 19.4 and 19.4.
+constexpr int kAcMinPart = 256;
 constexpr float kAcLazy = 8.0f;  // log2 headroom before the running maximum moves
 
 template <int D>
@@ -205,7 +210,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // p_j = 2^(sl2 s_j + neg) of a 32-column block of scores, packed to bf16 (P's
 // rounding: half a step of 2^-8 relative, of a weight in a sum whose divisor l
 // is the fp32 sum of the unrounded weights; the tensor pipe takes P and V in
-// one 16-bit type).  Returns the fp32 sum.  A masked score (-inf) gives 0.
+// one 16-bit type, and V comes out of its page as bf16 -- an fp16 P, as the
+// block attention keeps it, wants V converted in shared memory first, a pass
+// over every page for each tile pair).  Returns the fp32 sum.  A masked score (-inf) gives 0.
 __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], uint64_t sl2, uint64_t neg, uint32_t* pk) {
   uint64_t sum = pack2(0.f, 0.f), sum1 = sum;
 #pragma unroll

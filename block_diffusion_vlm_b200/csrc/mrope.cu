@@ -6,9 +6,11 @@
 // theta = pos[axis(j)][row] * base^(-2j/rot); elements from rot on pass
 // unchanged.  The angle is formed in turns, t = pos * (base^(-2j/rot) / 2 pi),
 // and reduced to t - rint(t) in fp64: positions of 10^5 keep an absolute error
-// near 1e-11 turns, where fp32 would lose the angle altogether.  The cosine
-// and sine of the reduced angle, the products and the sum are fp32; one
-// rounding at the store.
+// near 1e-11 turns, where fp32 would lose the angle altogether.  The reduced
+// angle is rounded to fp32 (half a step is at most 2^-26 turns, which moves its
+// cosine and sine by less than 1e-7, as much as the products' own roundings),
+// and the sine, the cosine, the products and the sum are fp32; one rounding at
+// the store.
 //
 // Bound: HBM (each element read once, written once).  A warp owns a row: it
 // sends out the loads of its first kMrBatch pieces per lane (16 bytes of each
@@ -23,7 +25,8 @@
 // Measured: 16384 rows of 16/2 heads of 128, 35.9 us (168 MB: 4.7 TB/s; a plain
 // copy of 80 MB to another 80 MB takes 27 us); 1357 rows of 14/2 heads of 64,
 // 5.4 us; one block of 16 rows, 3.1 us; 4999 rows of 16 heads of 80 in fp32,
-// 11.8 us.  Blocks of 256 threads: 38.0, 4.7, 3.5 and 12.0 us.  Value
+// 11.8 us, in bf16 8.0 us; 1357 rows of 16/2 heads of 128, 7.9 us, in a buffer
+// of 16384 rows with the rest padding 12.6 us.  Blocks of 256 threads: 38.0, 4.7, 3.5 and 12.0 us.  Value
 // tiles of 32 rows: 39.8 and 4.8 us for the first two.  Values turned by the
 // block that turns their rows, instead of by blocks of their own: 50 us.  Rows
 // brought in by bulk copies, a ring of rows per warp: 37 us.

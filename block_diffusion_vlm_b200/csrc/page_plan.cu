@@ -14,10 +14,13 @@
 // Bound: latency.  The outputs are 4 bytes a row and the inputs 8 bytes a
 // request; what takes time is the chain of lengths, scan, table entry, store.
 // One CTA holds small steps; from kPlanWide rows on the slot map is shared by
-// as many CTAs as have four rows a thread.  Where kv_len or free_count_out is
-// the input array, or held_len is updated, every CTA's reads have to come before the first write: then
-// the CTAs are one cluster of eight and meet at its barrier (144000 rows of
-// 512 requests: 20 us, against 7.5 us for a grid of 71).
+// as many CTAs as have four rows a thread (one CTA against the grid: 2085 rows
+// 5.4 and 5.2 us, 3237 rows 6.8 and 5.5, 4133 rows 7.1 and 5.6, 12837 rows 13.2
+// and 5.7).  Where kv_len or free_count_out is the input array, or held_len is
+// updated, every CTA's reads have to come before the first write: then the CTAs
+// are one cluster of eight and meet at its barrier (144000 rows of 512
+// requests: 27 us, against 8 us for a grid of 71; 165 rows of 8 requests 6 to 7
+// us, against 5.3).
 #include "ptx.cuh"
 #include "step.h"
 

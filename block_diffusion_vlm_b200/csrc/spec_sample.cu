@@ -344,9 +344,10 @@ cudaError_t launch_spec_sample(const SpecSampleArgs& a, bool is_bf16, cudaStream
                    (reinterpret_cast<uintptr_t>(a.draft_p) & 15u) == 0;
   // CTAs per sequence: as many as keep the batch within what the SMs hold at
   // once (two CTAs each), up to the portable cluster size; fewer for
-  // vocabularies that leave warps without a step of four pieces.  128 rows of
-  // 151936 in bf16: 16.8 us with 2 CTAs each; 28 us with 4 and 40 us with 8
-  // against 22 us with 2 in an earlier form
+  // vocabularies that leave warps without a step of four pieces.  Rows of
+  // 151936 with 1, 2, 4 and 8 CTAs each: one sequence of fp32 18.7, 12.4, 8.8
+  // and 7.4 us; 32 of bf16 17.0, 11.8, 9.4 and 9.8; 128 of bf16 20.3, 16.7, 23.4
+  // and 35.6; 64 of bf16 with the draft's rows 25.0, 16.6, 16.8 and 22.5
   const int steps = (a.V + 1023) / 1024, room = 2 * device_sm_count();
   int n_cta = 1;
   while (n_cta < kSvMaxCta && 2 * n_cta * a.b <= room && n_cta * kSvWarps / 4 < steps) n_cta *= 2;

@@ -322,9 +322,12 @@ DVLM_API dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new
  * first rot_dim elements of each head turn in pairs (j, j + rot_dim / 2) by
  * pos[axis(j)][row] * rope_base^(-2j / rot_dim); the rest passes unchanged.
  * pos [n_axes, n_rows]: device int32, any sign.  sections (HOST int [n_axes],
- * sum rot_dim / 2): how many frequencies each axis takes -- in order, axis 0's
- * first (interleaved = 0), or interleaved = 1: frequency j goes to axis j %
- * n_axes while j < n_axes * sections of that axis, else to axis 0.  Angles are
+ * sum rot_dim / 2): interleaved = 0: how many frequencies each axis takes, in
+ * order, axis 0's first.  interleaved = 1: frequency j goes to axis j % n_axes
+ * while j < n_axes * sections of that axis, else to axis 0 -- an axis behind
+ * axis 0 takes its section or as many frequencies as fall to it, whichever is
+ * less, and axis 0 all others ((16, 24, 24) at rot_dim 128: 22, 21 and 21, for
+ * there are no 24 frequencies to either).  Angles are
  * reduced in fp64; products in fp32; one rounding to the output.  With one
  * axis and rot_dim = D this is the model's own rotate-half RoPE.
  * x, out: n_rows rows of n_heads heads of D, row strides x_ld, out_ld
