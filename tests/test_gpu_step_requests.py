@@ -324,3 +324,29 @@ def test_two_batches_at_once_all_steps(cuda):
             assert torch.equal(getattr(x, k), getattr(y, k)), k
         for k in ("q", "out", "kp", "vp"):
             assert torch.equal(getattr(x, k).view(torch.int16), getattr(y, k).view(torch.int16)), k
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 151936), (torch.bfloat16, 50257)])
+@pytest.mark.parametrize("b", [1, 5])
+def test_sequences_without_rows_among_large_vocabularies(cuda, dtype, V, b):
+    """Several CTAs a sequence: the ones that have nothing to do leave, the others' tokens are right."""
+    K = 4
+    g = torch.Generator().manual_seed(b)
+    p = torch.softmax(2.0 * torch.randn(b, K + 1, V, generator=g), -1).to(dtype)
+    q = torch.softmax(2.0 * torch.randn(b, K, V, generator=g), -1).to(dtype)
+    ids, u, us = torch.randint(0, V, (b, K), generator=g), torch.rand(b, K, generator=g), torch.rand(b, generator=g)
+    for rows in ([0] * b, [5] * b, [5 * (i % 2) for i in range(b)]):
+        acc, tok, cache, st = i32([9] * b, cuda), i32([[9] * (K + 1)] * b, cuda), i32([100] * b, cuda), status(cuda)
+        dv.spec_verify_sample(p.to(cuda), q.to(cuda), ids.to(torch.int32).to(cuda), u.to(cuda), us.to(cuda), b=b, K=K,
+                              V=V, dtype=dv.DVLM_FP32 if dtype == torch.float32 else dv.DVLM_BF16, accept_len=acc,
+                              out_ids=tok, cache_len=cache, cache_len_out=cache,
+                              cu_rows=i32(np.concatenate([[0], np.cumsum(rows)]), cuda), status=st)
+        assert_ok(st)
+        for i in range(b):
+            want = (0, [-1] * (K + 1), 100)
+            if rows[i]:
+                k, out, bad = ref.verify(p[i].double().numpy(), q[i].double().numpy(), ids[i].tolist(),
+                                         u[i].double().numpy(), float(us[i]), K)
+                assert not bad
+                want = (k, out, 100 - (K - k))
+            assert (int(acc[i]), tok[i].tolist(), int(cache[i])) == want
