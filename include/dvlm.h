@@ -301,14 +301,15 @@ DVLM_API dvlm_status dvlm_spec_verify_accept(const void* verify_logits, const in
  * as cache_len), and sets it to the larger of itself and
  * kv_len (0 for a finished request).  kv_len may be cache_len and
  * free_count_out may be free_count; no other arrays may overlap.  A request whose cached
- * length is outside 0 .. 64 max_pages, whose held length is above that, whose new length is below -1, or whose sum is
- * past 64 max_pages takes no part (kv_len: its cached length in the last case; 0
- * in the others, or left as it is where kv_len is cache_len) and sets DVLM_ERR_BOUNDS, as does a free_count
+ * length is outside 0 .. 64 max_pages, whose held length is above that, whose
+ * new length is below -1, or whose sum is past 64 max_pages takes no part
+ * (kv_len: its cached length in the last case; 0 in the others, or left as it
+ * is where kv_len is cache_len) and sets DVLM_ERR_BOUNDS, as does a free_count
  * outside 0 .. n_pages (cut to it) or a stack that would pass n_pages.  Page
  * numbers are passed on as they are (in slot_map cut to +- (2^25 - 1), past any
  * store, and -1 taken for -2): a row on a number that is no page of the store
- * never has slot -1, so that dvlm_mrope_append_paged reports it.  All pointers device int32.  n_batch <=
- * 4096, n_pages and max_pages < 2^25, n_batch * max_pages < 2^31, max_rows <=
+ * never has slot -1, so that dvlm_mrope_append_paged reports it.  All pointers
+ * device int32.  n_batch <= 4096, n_pages and max_pages < 2^25, n_batch * max_pages < 2^31, max_rows <=
  * 2^30.  Errors: INVALID_ARG, SHAPE.  One
  * launch, no workspace. */
 DVLM_API dvlm_status dvlm_page_plan(const int32_t* cache_len, const int32_t* new_len, int32_t* block_table,
@@ -378,8 +379,8 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
  * scale > 0 (scale * log2(e) a finite fp32).  Hidden slots and
  * those at or beyond kv_len[b] may hold anything, NaN included; the slots
  * between must be finite.  A query that holds a NaN, or an infinity that meets
- * keys of both signs, gives NaN in its row of out and lse, and in no other.  Scores, softmax and sums in fp32, P in bf16.  The
- * other requests of a call move the cuts of a request's work, and with them the
+ * keys of both signs, gives NaN in its row of out and lse, and in no other.
+ * Scores, softmax and sums in fp32, P in bf16.  The other requests of a call move the cuts of a request's work, and with them the
  * order of its fp32 sums and the reference maxima against which P is rounded:
  * alone and in a batch a row differs by at most twice P's rounding (2^-8 of
  * sum_j p_j |v_j| / sum_j p_j either side) and the store's.  The same call
@@ -423,8 +424,8 @@ DVLM_API dvlm_status dvlm_chunk_attn_paged(const void* q, void* out, const void*
  * [0, 1) counts as the nearest value inside.  If r is 0 everywhere the draw is
  * from the target row itself; if that is 0 too, token 0 and DVLM_ERR_BOUNDS.
  * A draft outside 0..V-1 is refused (DVLM_ERR_BOUNDS; behind a refused draft
- * none is looked at), as is an n_draft outside 0..K (cut to it).  1 <= K <= 64, b <= 65535, V <= 2^30.  Sums and
- * decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace.
+ * none is looked at), as is an n_draft outside 0..K (cut to it).  1 <= K <= 64,
+ * b <= 65535, V <= 2^30.  Sums and decisions in fp64.  Errors: INVALID_ARG, SHAPE.  One launch, no workspace.
  *
  * Behind dvlm_page_plan use the _rows form: it takes the plan's cu_rows [b + 1]
  * (device int32), for only the device knows which requests got their rows.  A
