@@ -381,10 +381,11 @@ DVLM_API dvlm_status dvlm_mrope_append_paged(const void* qkv, const int32_t* pos
  * between must be finite.  A query that holds a NaN, or an infinity that meets
  * keys of both signs, gives NaN in its row of out and lse, and in no other.
  * Scores, softmax and sums in fp32, P in bf16.  The other requests of a call
- * move the cuts of a request's work, and with them the order of its fp32 sums and the reference maxima against which P is rounded:
- * alone and in a batch a row differs by at most twice P's rounding (2^-8 of
- * sum_j p_j |v_j| / sum_j p_j either side) and the store's.  The same call
- * gives the same bits.  A request whose
+ * move the cuts of a request's work, and with them the order of its fp32 sums
+ * and the reference maxima against which P is rounded: alone and in a batch a
+ * row differs by at most twice P's rounding (2^-8 of sum_j p_j |v_j| / sum_j
+ * p_j either side) and the store's.  The same call gives the same bits.  A
+ * request whose
  * cu_rows descend or leave 0 .. n_rows, whose kv_len is outside 0 .. 64
  * max_pages or below n_b, takes no part (DVLM_ERR_BOUNDS); a page number
  * outside 0 .. n_pages - 1 sets DVLM_ERR_BOUNDS and page 0 is read.  cu_rows,
